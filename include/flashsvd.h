@@ -327,6 +327,105 @@ FLASHSVD_API int flashsvd_prefill_attn_factorized(const flashsvd_bf16* z_q, cons
                                                   int B, int S, int H, int D, int S_max, int r,
                                                   int causal, float scale, flashsvd_stream stream);
 
+/* ------------------------------------------------ 8-bit key/value cache --
+ * No counterpart in the pages: a dense cache in half the bytes, the decode
+ * attention that reads it, and the eviction of tokens that attention hardly
+ * uses.
+ *
+ * Tokens are grouped into blocks of FLASHSVD_KV8_BLOCK = 64.  A block of one
+ * KV head is held as 8-bit codes (int8, or e4m3) with one fp32 scale 2^e: e
+ * is the least integer with max |x| <= LIM 2^e (LIM = 127 for int8, 448 for
+ * e4m3), and at least -100; code = x / 2^e rounded to nearest, ties to even;
+ * value = code * 2^e.  A block that holds an infinity or a NaN gets the
+ * scale NaN and codes 0 (everything that reads it becomes NaN).  A block is
+ * quantised once, when its 64th row arrives; the rows of the block that
+ * holds the newest token are (also) kept in a bf16 tail, and attention reads
+ * that block from the tail.  The cache after n rows is therefore the same
+ * however they arrived.
+ *
+ * flashsvd_kv8 (host struct of device pointers):
+ *   k, v             [B, H_kv, S_max, D] codes
+ *   k_scale, v_scale [B, H_kv, S_max / 64] fp32
+ *   k_tail, v_tail   [B, H_kv, 64, D] bf16
+ * S_max a multiple of 64, D in {64, 128}, B * H_kv <= 65535.  H_kv may be
+ * smaller than the number of query heads H (H a multiple of it; query head h
+ * reads KV head h / (H / H_kv)).
+ */
+#define FLASHSVD_KV8_BLOCK 64
+enum flashsvd_kv8_format { FLASHSVD_KV8_INT8 = 0, FLASHSVD_KV8_E4M3 = 1 };
+typedef struct flashsvd_kv8 {
+  int format;                   /* enum flashsvd_kv8_format */
+  int B, H_kv, D, S_max;
+  uint8_t* k; uint8_t* v;
+  float* k_scale; float* v_scale;
+  flashsvd_bf16* k_tail; flashsvd_bf16* v_tail;
+} flashsvd_kv8;
+
+/* Store a prompt: rows 0..n-1 of k_rows / v_rows [B, S_src, H_kv, D] (the
+ * layout of the dense caches above; S <= S_src rows are used) become tokens
+ * 0..n-1 of the cache, n = lens[b] (device int32[B], clamped to [0, S]) or S
+ * when lens is NULL.  Rows at or beyond n are not read, and no block, scale
+ * or tail slot beyond them is written.  S <= cache S_max. */
+FLASHSVD_API int flashsvd_kv8_store(const flashsvd_bf16* k_rows, const flashsvd_bf16* v_rows,
+                                    const flashsvd_kv8* cache, const int32_t* lens, int S, int S_src,
+                                    flashsvd_stream stream);
+
+/* One decode step, as flashsvd_dense_kv_decode_attn: k_new and v_new (each
+ * [B x H_kv x D], both or neither NULL) become token cache_seqlens[b], then
+ * q [B x H x D] attends over tokens 0..cache_seqlens[b] (device int32[B];
+ * clamped to [0, S_max - 1]; not incremented; the tail must hold the rows of
+ * that token's block).  out [B x H x D] bf16.
+ * weights (fp32 [B, H_kv, S_max], or NULL) receives the attention weight of
+ * every token j <= cache_seqlens[b], summed over the query heads of the KV
+ * head: added to it when accumulate != 0 (the entry of a token appended by
+ * this call is set, not added to), written when accumulate is 0.  Entries
+ * beyond cache_seqlens[b] are left alone.
+ * At most 16 query heads per KV head, B <= 1024.  With weights, H * S_max
+ * floats of the context's workspace (64 MiB) hold one batch row's scores: a
+ * call with a larger row returns FLASHSVD_ERR_UNSUPPORTED_SHAPE. */
+FLASHSVD_API int flashsvd_kv8_decode_attn(const flashsvd_bf16* q, const flashsvd_bf16* k_new,
+                                          const flashsvd_bf16* v_new, const flashsvd_kv8* cache,
+                                          const int32_t* cache_seqlens, float* weights, int accumulate,
+                                          flashsvd_bf16* out, int H, float scale,
+                                          flashsvd_stream stream);
+
+/* Causal attention weight that the tokens of a prompt receive from its last
+ * `window` queries, summed over the query heads of each KV head:
+ *   weights[b, g, j] = sum_{h in g} sum_{i = max(j, n - window)}^{n - 1}
+ *                      softmax_{j' <= i}(q[b,i,h] . k[b,j',g] * scale)_j,  j < n,
+ * n = lens[b] (device int32[B], clamped to [0, S]) or S when lens is NULL.
+ * q [B, S, H, D]; keys are rows of k_cache [B, S_max, H_kv, D]; weights fp32
+ * [B, H_kv, w_stride], w_stride >= S; entries at or beyond n are left alone,
+ * and rows of q and k at or beyond n may hold anything.  window >= 1 (at or
+ * above S: every query).  D in {64, 128}.  The workspace holds 4 bytes per
+ * (query of the window, head): B * H * min(window, S) up to about 16 million;
+ * above that FLASHSVD_ERR_UNSUPPORTED_SHAPE. */
+FLASHSVD_API int flashsvd_attn_weight_sums(const flashsvd_bf16* q, const flashsvd_bf16* k_cache,
+                                           float* weights, const int32_t* lens, int B, int S, int H,
+                                           int H_kv, int D, int S_max, int w_stride, int window,
+                                           float scale, flashsvd_stream stream);
+
+/* Keep `keep` tokens of every (batch row, KV head) with more: the `recent`
+ * newest, and of the others the keep - recent with the largest weights_in
+ * (fp32 [B, H_kv, src S_max]; ties to the lower index, NaN below every
+ * number), in their order.  seqlens_in[b] counts the tokens in src (device
+ * int32[B], clamped to [0, S_max]).  The kept rows become tokens 0..m-1 of
+ * dst, m = min(keep, seqlens_in[b]), their weights weights_out (fp32
+ * [B, H_kv, dst S_max]), m seqlens_out[b] (NULL: not written), and kept
+ * (device int32 [B, H_kv, keep]) the indices they had, -1 from m on.
+ * Rows keep the values they had in src; their blocks are formed anew (a
+ * block with a smaller largest value gets finer codes, one with a larger
+ * coarser ones).  Nothing beyond m is written.
+ * dst may be src itself (every pointer of the two equal; weights_out then
+ * is weights_in): eviction in place.  Otherwise no buffer of dst, and not
+ * weights_out, may overlap src.  seqlens_out may be seqlens_in.
+ * 1 <= keep <= dst S_max, keep <= src S_max, 0 <= recent <= keep; src and
+ * dst of one format, B, H_kv and D. */
+FLASHSVD_API int flashsvd_kv8_evict(const flashsvd_kv8* src, const flashsvd_kv8* dst,
+                                    const float* weights_in, float* weights_out,
+                                    const int32_t* seqlens_in, int32_t* seqlens_out, int32_t* kept,
+                                    int keep, int recent, flashsvd_stream stream);
+
 /* --------------------------------------------------------------- glue ----
  * RMSNorm y = x * g / sqrt(mean(x^2) + eps); LayerNorm
  * y = (x - mean) / sqrt(var + eps) * g + b (population variance).  Rows of

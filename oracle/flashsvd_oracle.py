@@ -330,3 +330,82 @@ def widen_layer(w_bf16: dict) -> dict:
         else:
             out[k] = v
     return out
+
+
+# ------------------------------------------------- 8-bit key/value cache --
+# No counterpart in the pages; the definitions are those of include/flashsvd.h.
+
+KV8_BLOCK = 64
+KV8_LIMIT = {"int8": 127.0, "e4m3": 448.0}
+
+
+def kv8_exponent(amax: float, fmt: str) -> int:
+    """Least integer e >= -100 with amax <= LIM 2^e."""
+    e = -100
+    while amax > KV8_LIMIT[fmt] * 2.0 ** e:
+        e += 1
+    return e
+
+
+def kv8_round(y, fmt: str):
+    """Nearest code, ties to even: integers, or e4m3 numbers (a leading bit
+    and three more, spacing 2^-9 below 2^-6)."""
+    y = np.asarray(y, np.float64)
+    if fmt == "int8":
+        return np.rint(y)
+    a = np.maximum(np.abs(y), 2.0 ** -6)
+    step = 2.0 ** (np.floor(np.log2(a)) - 3)
+    return np.rint(y / step) * step
+
+
+def kv8_block(rows, fmt: str):
+    """(codes, scale) of one block of rows of one head."""
+    rows = np.asarray(rows, np.float64)
+    if not np.all(np.isfinite(rows)):
+        return np.zeros_like(rows), math.nan
+    s = 2.0 ** kv8_exponent(float(np.max(np.abs(rows))), fmt)
+    return kv8_round(rows / s, fmt), s
+
+
+def kv8_rows(rows, fmt: str):
+    """The values that the cache holds of rows [n, D] of one head: full blocks
+    but the newest token's quantised, that one as it is."""
+    out = np.array(rows, np.float64)
+    n = out.shape[0]
+    for b in range((n - 1) // KV8_BLOCK):
+        sl = slice(b * KV8_BLOCK, (b + 1) * KV8_BLOCK)
+        codes, s = kv8_block(out[sl], fmt)
+        out[sl] = codes * s
+    return out
+
+
+def attention_probs(q, k, scale):
+    """softmax(q k^T scale) of queries q [m, D] over keys k [n, D]."""
+    x = np.asarray(q, np.float64) @ np.asarray(k, np.float64).T * scale
+    e = np.exp(x - x.max(axis=-1, keepdims=True))
+    return e / e.sum(axis=-1, keepdims=True)
+
+
+def attn_weight_sums(q, k, window, scale):
+    """Causal attention weight of each key of k [n, D] from the last `window`
+    queries of q [n, heads, D], summed over the heads."""
+    q, k = np.asarray(q, np.float64), np.asarray(k, np.float64)
+    n = k.shape[0]
+    w = np.zeros(n)
+    for i in range(max(0, n - window), n):
+        w[: i + 1] += attention_probs(q[i], k[: i + 1], scale).sum(axis=0)
+    return w
+
+
+def evict_kept(weights, keep, recent):
+    """Indices kept of n tokens: the `recent` newest and, of the others, the
+    keep - recent with the largest weights (ties to the lower index, NaN below
+    every number), in ascending order."""
+    w = np.asarray(weights, np.float64)
+    n = w.shape[0]
+    if n <= keep:
+        return np.arange(n)
+    old = n - recent
+    order = sorted(range(old), key=lambda i: (not math.isnan(w[i]), 0.0 if math.isnan(w[i]) else w[i], -i),
+                   reverse=True)
+    return np.array(sorted(order[: keep - recent]) + list(range(old, n)), np.int64)

@@ -270,6 +270,23 @@ int check_layer(const flashsvd_layer* L) {
   return FLASHSVD_OK;
 }
 
+int check_kv8(const flashsvd_kv8* c, Kv8* out) {
+  if (!c) return FLASHSVD_ERR_INVALID_ARG;
+  if (c->format != FLASHSVD_KV8_INT8 && c->format != FLASHSVD_KV8_E4M3) return FLASHSVD_ERR_INVALID_ARG;
+  if (c->B < 0 || c->H_kv <= 0 || c->S_max <= 0) return FLASHSVD_ERR_INVALID_ARG;
+  if (c->D != 64 && c->D != 128) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
+  if (c->S_max % KV8_BLOCK || (long long)c->B * c->H_kv > 65535) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
+  const void* ptrs[] = {c->k, c->v, c->k_scale, c->v_scale, c->k_tail, c->v_tail};
+  for (const void* q : ptrs) FSVD_TRY(check_ptr(q));
+  out->e4m3 = c->format == FLASHSVD_KV8_E4M3;
+  out->B = c->B; out->G = c->H_kv; out->D = c->D; out->S_max = c->S_max;
+  out->codes[0] = c->k; out->codes[1] = c->v;
+  out->scale[0] = c->k_scale; out->scale[1] = c->v_scale;
+  out->tail[0] = reinterpret_cast<bf16*>(c->k_tail);
+  out->tail[1] = reinterpret_cast<bf16*>(c->v_tail);
+  return FLASHSVD_OK;
+}
+
 PfLinear pf_base(const bf16* x, long long ldx, const flashsvd_factor& F, int M,
                  int d, int n, bf16* y, long long ldy) {
   PfLinear p;
@@ -994,6 +1011,90 @@ int flashsvd_prefill_attn_factorized(const flashsvd_bf16* z_q, const flashsvd_bf
   a.rope_cos = rope_cos; a.rope_sin = rope_sin;
   // the caller's z_q is an input: it is not discarded from L2
   return attn_prefill_launch(a, stream);
+}
+
+int flashsvd_kv8_store(const flashsvd_bf16* k_rows, const flashsvd_bf16* v_rows, const flashsvd_kv8* cache,
+                       const int32_t* lens, int S, int S_src, flashsvd_stream stream) {
+  Kv8 c;
+  FSVD_TRY(check_kv8(cache, &c));
+  FSVD_TRY(check_ptr(k_rows)); FSVD_TRY(check_ptr(v_rows));
+  if (S < 0 || S_src < S || S > c.S_max) return FLASHSVD_ERR_INVALID_ARG;
+  if (c.B == 0 || S == 0) return FLASHSVD_OK;
+  return kv8_store_launch(cb(k_rows), cb(v_rows), c, lens, S, S_src, stream);
+}
+
+int flashsvd_kv8_decode_attn(const flashsvd_bf16* q, const flashsvd_bf16* k_new, const flashsvd_bf16* v_new,
+                             const flashsvd_kv8* cache, const int32_t* cache_seqlens, float* weights,
+                             int accumulate, flashsvd_bf16* out, int H, float scale, flashsvd_stream stream) {
+  FSVD_TRY(need_init());
+  Kv8AttnParams a;
+  memset(&a, 0, sizeof(a));
+  FSVD_TRY(check_kv8(cache, &a.c));
+  FSVD_TRY(check_ptr(q)); FSVD_TRY(check_ptr(out));
+  if (!cache_seqlens || (k_new == nullptr) != (v_new == nullptr)) return FLASHSVD_ERR_INVALID_ARG;
+  FSVD_TRY(check_opt_ptr(k_new)); FSVD_TRY(check_opt_ptr(v_new)); FSVD_TRY(check_opt_ptr(weights));
+  if (H <= 0 || H % a.c.G || !(scale > 0.f)) return FLASHSVD_ERR_INVALID_ARG;
+  if (H / a.c.G > 16) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
+  if (a.c.B == 0) return FLASHSVD_OK;
+  a.q = cb(q); a.k_new = cb(k_new); a.v_new = cb(v_new);
+  a.seqlens = cache_seqlens;
+  a.weights = weights; a.accumulate = accumulate != 0;
+  a.out = (bf16*)out;
+  a.H = H;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.part = cur().apart; a.part_cap = (long long)cur().apart_elems;
+  a.counters = cur().acounters; a.counters_cap = kCountersN;
+  return kv8_attn_launch(a, cur().sm_count, stream);
+}
+
+int flashsvd_attn_weight_sums(const flashsvd_bf16* q, const flashsvd_bf16* k_cache, float* weights,
+                              const int32_t* lens, int B, int S, int H, int H_kv, int D, int S_max,
+                              int w_stride, int window, float scale, flashsvd_stream stream) {
+  FSVD_TRY(need_init());
+  FSVD_TRY(check_ptr(q)); FSVD_TRY(check_ptr(k_cache)); FSVD_TRY(check_ptr(weights));
+  if (B < 0 || S < 0 || H <= 0 || H_kv <= 0 || H % H_kv || S_max < S || w_stride < S || window < 1 ||
+      !(scale > 0.f))
+    return FLASHSVD_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
+  if (B == 0 || S == 0) return FLASHSVD_OK;
+  AttnSumsParams a;
+  memset(&a, 0, sizeof(a));
+  a.q = cb(q); a.k = cb(k_cache); a.weights = weights; a.lens = lens;
+  a.B = B; a.S = S; a.H = H; a.G = H_kv; a.D = D; a.S_max = S_max; a.w_stride = w_stride; a.window = window;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.ws = cur().apart; a.ws_cap = (long long)cur().apart_elems;
+  a.counters = cur().acounters; a.counters_cap = kCountersN;
+  a.status = cur().status;
+  return attn_sums_launch(a, cur().sm_count, stream);
+}
+
+int flashsvd_kv8_evict(const flashsvd_kv8* src, const flashsvd_kv8* dst, const float* weights_in,
+                       float* weights_out, const int32_t* seqlens_in, int32_t* seqlens_out, int32_t* kept,
+                       int keep, int recent, flashsvd_stream stream) {
+  FSVD_TRY(need_init());
+  Kv8EvictParams a;
+  memset(&a, 0, sizeof(a));
+  FSVD_TRY(check_kv8(src, &a.src)); FSVD_TRY(check_kv8(dst, &a.dst));
+  FSVD_TRY(check_ptr(weights_in)); FSVD_TRY(check_ptr(weights_out));
+  if (!seqlens_in || !kept) return FLASHSVD_ERR_INVALID_ARG;
+  if (a.src.e4m3 != a.dst.e4m3 || a.src.B != a.dst.B || a.src.G != a.dst.G || a.src.D != a.dst.D)
+    return FLASHSVD_ERR_INVALID_ARG;
+  if (keep < 1 || keep > a.src.S_max || keep > a.dst.S_max || recent < 0 || recent > keep)
+    return FLASHSVD_ERR_INVALID_ARG;
+  // in place: all of src's buffers, or none of them
+  int same = weights_in == weights_out;
+  for (int x = 0; x < 2; ++x)
+    same += (a.src.codes[x] == a.dst.codes[x]) + (a.src.scale[x] == a.dst.scale[x]) +
+            (a.src.tail[x] == a.dst.tail[x]);
+  if (same != 0 && same != 7) return FLASHSVD_ERR_INVALID_ARG;
+  if (same == 7 && a.src.S_max != a.dst.S_max) return FLASHSVD_ERR_INVALID_ARG;
+  if (a.src.B == 0) return FLASHSVD_OK;
+  a.w_in = weights_in; a.w_out = weights_out;
+  a.n_in = seqlens_in; a.n_out = seqlens_out; a.kept = kept;
+  a.keep = keep; a.recent = recent; a.in_place = same == 7;
+  a.ws = reinterpret_cast<int*>(cur().apart); a.ws_cap = (long long)cur().apart_elems;
+  a.status = cur().status;
+  return kv8_evict_launch(a, stream);
 }
 
 int flashsvd_rmsnorm(const flashsvd_bf16* x, const flashsvd_bf16* g,

@@ -189,4 +189,59 @@ struct AttnPfParams {
 };
 int attn_prefill_launch(const AttnPfParams& p, cudaStream_t stream);
 
+// ------------------------------------------------ 8-bit key/value cache ----
+constexpr int KV8_BLOCK = FLASHSVD_KV8_BLOCK;  // tokens of a block
+
+struct Kv8 {
+  int e4m3;                      // codes: e4m3 (1) or int8 (0)
+  int B, G, D, S_max;            // G KV heads; S_max a multiple of KV8_BLOCK
+  uint8_t* codes[2];             // k, v [B, G, S_max, D]
+  float* scale[2];               // [B, G, S_max / KV8_BLOCK]
+  bf16* tail[2];                 // [B, G, KV8_BLOCK, D]
+};
+
+// Rows [B, S_src, G, D] -> the cache; lens[b] of them (null: S).
+int kv8_store_launch(const bf16* k, const bf16* v, const Kv8& c, const int* lens, int S, int S_src,
+                     cudaStream_t stream);
+
+struct Kv8AttnParams {
+  const bf16* q; const bf16* k_new; const bf16* v_new;
+  Kv8 c;
+  const int* seqlens;
+  float* weights; int accumulate;  // [B, G, S_max], or null
+  bf16* out;
+  int H;
+  float scale_log2;                // scale * log2(e)
+  float* part; long long part_cap; // workspace (floats)
+  int* counters; int counters_cap; // zero between launches
+};
+constexpr int KV8_MAX_BATCH = 1024;  // batch entries of one attention call
+int kv8_attn_launch(const Kv8AttnParams& p, int sm_count, cudaStream_t stream);
+
+struct Kv8EvictParams {
+  Kv8 src, dst;                    // dst may be src (in place)
+  const float* w_in; float* w_out; // [B, G, S_max] of src / of dst
+  const int* n_in; int* n_out;     // n_out may be null
+  int* kept;                       // [B, G, keep]
+  int keep, recent;
+  int in_place;
+  int* ws; long long ws_cap;       // workspace (ints)
+  int* status;
+};
+int kv8_evict_launch(const Kv8EvictParams& p, cudaStream_t stream);
+
+// ------------------------------------------- attention weight per key ------
+struct AttnSumsParams {
+  const bf16* q;                   // [B, S, H, D]
+  const bf16* k;                   // [B, S_max, G, D]
+  float* weights;                  // [B, G, w_stride]
+  const int* lens;                 // [B] or null
+  int B, S, H, G, D, S_max, w_stride, window;
+  float scale_log2;
+  float* ws; long long ws_cap;     // workspace (floats)
+  int* counters; int counters_cap; // zero between launches
+  int* status;
+};
+int attn_sums_launch(const AttnSumsParams& p, int sm_count, cudaStream_t stream);
+
 }  // namespace fsvd

@@ -1,0 +1,106 @@
+// A prompt's key and value rows into the 8-bit cache.
+//
+// One CTA per (batch row, 64-token block, KV head) takes the block's 64 rows
+// of K and V, half of its threads each: every thread holds its share of the
+// rows in registers (all loads in flight at once), the threads of a tensor
+// agree on the largest magnitude, and each writes its codes.  Every byte is
+// read and written once; the kernel is bound by HBM.
+#include "kv8.cuh"
+
+namespace fsvd {
+namespace {
+
+constexpr int ST_THREADS = 256;  // 128 for K, 128 for V
+
+struct StoreParams {
+  const bf16* src[2];
+  Kv8 c;
+  const int* lens;
+  int S, S_src, nblk;
+};
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(ST_THREADS)
+kv8_store_kernel(const __grid_constant__ StoreParams p) {
+  constexpr int UPR = D / 16;                 // units of 16 elements per row
+  constexpr int PER = KV8_BLOCK * UPR / 128;  // units per thread
+  __shared__ uint32_t s_max[ST_THREADS / 32];
+  const int tid = threadIdx.x, x = tid >> 7, t = tid & 127;
+  // heads fastest: neighbouring CTAs read neighbouring parts of the same rows
+  const int g = blockIdx.x % p.c.G, rest = blockIdx.x / p.c.G;
+  const int blk = rest % p.nblk, b = rest / p.nblk;
+
+  pdl_launch_dependents();
+  pdl_wait();
+
+  int n = p.lens ? p.lens[b] : p.S;
+  n = n < 0 ? 0 : (n > p.S ? p.S : n);
+  const int row0 = blk * KV8_BLOCK;
+  if (row0 >= n) return;
+  const int rows = min(KV8_BLOCK, n - row0);
+  const bool newest = row0 + KV8_BLOCK >= n;
+  const long long GD = (long long)p.c.G * D;
+  const bf16* src = p.src[x] + ((long long)b * p.S_src + row0) * GD + (long long)g * D;
+  uint4 a[PER], c[PER];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int u = t + 128 * i, r = u / UPR, col = (u % UPR) * 16;
+    a[i] = c[i] = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      a[i] = ld_once(src + r * GD + col);
+      c[i] = ld_once(src + r * GD + col + 8);
+    }
+  }
+  const long long pair = (long long)b * p.c.G + g;
+  if (rows == KV8_BLOCK) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) m = max(m, max(amax8(a[i]), amax8(c[i])));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((tid & 31) == 0) s_max[tid >> 5] = m;
+    __syncthreads();
+    m = max(max(s_max[4 * x], s_max[4 * x + 1]), max(s_max[4 * x + 2], s_max[4 * x + 3]));
+    const int e = kv8_exponent<E4M3>(m);
+    const bool fin = kv8_finite(m);
+    uint8_t* dst = p.c.codes[x] + (pair * p.c.S_max + row0) * D;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      *reinterpret_cast<uint4*>(dst + (t + 128 * i) * 16) = kv8_encode16<E4M3>(a[i], c[i], exp2i(-e), fin);
+    if (t == 0) p.c.scale[x][pair * (p.c.S_max / KV8_BLOCK) + blk] = kv8_scale(e, fin);
+  }
+  if (newest) {
+    bf16* tail = p.c.tail[x] + pair * KV8_BLOCK * D;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int u = t + 128 * i;
+      if (u / UPR < rows) {
+        *reinterpret_cast<uint4*>(tail + u * 16) = a[i];
+        *reinterpret_cast<uint4*>(tail + u * 16 + 8) = c[i];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+int kv8_store_launch(const bf16* k, const bf16* v, const Kv8& c, const int* lens, int S, int S_src,
+                     cudaStream_t stream) {
+  StoreParams p;
+  p.src[0] = k; p.src[1] = v;
+  p.c = c;
+  p.lens = lens; p.S = S; p.S_src = S_src;
+  p.nblk = ceil_div(S, KV8_BLOCK);
+  const long long ctas = (long long)c.B * c.G * p.nblk;
+  if (ctas > 0x7fffffffLL) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
+  const LaunchTag tag{"kv8_store", 6.0 * c.B * c.G * (double)S * c.D, 0.0};
+  const dim3 grid((unsigned)ctas), block(ST_THREADS);
+  if (c.D == 128)
+    return c.e4m3 ? launch_pdl(tag, kv8_store_kernel<128, true>, grid, block, 0, stream, p)
+                  : launch_pdl(tag, kv8_store_kernel<128, false>, grid, block, 0, stream, p);
+  if (c.D == 64)
+    return c.e4m3 ? launch_pdl(tag, kv8_store_kernel<64, true>, grid, block, 0, stream, p)
+                  : launch_pdl(tag, kv8_store_kernel<64, false>, grid, block, 0, stream, p);
+  return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
+}
+
+}  // namespace fsvd

@@ -31,6 +31,8 @@ STATUS_NAMES = {
 }
 DECODER, ENCODER = 0, 1
 PREFILL_CAUSAL, DECODE, ENCODER_BIDIR = 0, 1, 2
+KV8_INT8, KV8_E4M3 = 0, 1
+KV8_BLOCK = 64
 
 _p = C.c_void_p
 _i = C.c_int
@@ -60,6 +62,13 @@ class Layer(C.Structure):
         ("up", Factor), ("down", Factor),
         ("rope_cos", _p), ("rope_sin", _p),
         ("decode_pack", _p),
+    ]
+
+
+class Kv8(C.Structure):
+    _fields_ = [
+        ("format", _i), ("B", _i), ("H_kv", _i), ("D", _i), ("S_max", _i),
+        ("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("k_tail", _p), ("v_tail", _p),
     ]
 
 
@@ -96,6 +105,10 @@ _SIGS = {
     "flashsvd_prefill_attn": ([_p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _f, _p], _i),
     "flashsvd_prefill_attn_factorized": ([_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i,
                                           _f, _p], _i),
+    "flashsvd_kv8_store": ([_p, _p, C.POINTER(Kv8), _p, _i, _i, _p], _i),
+    "flashsvd_kv8_decode_attn": ([_p, _p, _p, C.POINTER(Kv8), _p, _p, _i, _p, _i, _f, _p], _i),
+    "flashsvd_attn_weight_sums": ([_p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p], _i),
+    "flashsvd_kv8_evict": ([C.POINTER(Kv8), C.POINTER(Kv8), _p, _p, _p, _p, _p, _i, _i, _p], _i),
     "flashsvd_rmsnorm": ([_p, _p, _p, _i, _i, _f, _p], _i),
     "flashsvd_layernorm": ([_p, _p, _p, _p, _i, _i, _f, _p], _i),
     "flashsvd_rope_table": ([_p, _p, _i, _i, _f, _p], _i),
@@ -300,6 +313,35 @@ def prefill_attn_factorized(z_q, V_q, rope_cos, rope_sin, k_cache, v_cache, out,
     _call("flashsvd_prefill_attn_factorized", ptr(z_q), ptr(V_q), ptr(rope_cos), ptr(rope_sin),
           ptr(k_cache), ptr(v_cache), ptr(out), B, S, H, D, S_max, r, int(causal), scale,
           stream_handle(stream))
+
+
+def _kv8(cache):
+    """The flashsvd_kv8 struct of a cache (kv8.KV8Cache or the struct itself)."""
+    return cache if isinstance(cache, Kv8) else cache.struct
+
+
+def kv8_store(k_rows, v_rows, cache, lens, S, S_src, stream=None):
+    _call("flashsvd_kv8_store", ptr(k_rows), ptr(v_rows), _kv8(cache), ptr(lens), S, S_src,
+          stream_handle(stream))
+
+
+def kv8_decode_attn(q, k_new, v_new, cache, cache_seqlens, weights, accumulate, out, H, scale,
+                    stream=None):
+    _call("flashsvd_kv8_decode_attn", ptr(q), ptr(k_new), ptr(v_new), _kv8(cache),
+          ptr(cache_seqlens), ptr(weights), int(accumulate), ptr(out), H, scale,
+          stream_handle(stream))
+
+
+def attn_weight_sums(q, k_cache, weights, lens, B, S, H, H_kv, D, S_max, w_stride, window, scale,
+                     stream=None):
+    _call("flashsvd_attn_weight_sums", ptr(q), ptr(k_cache), ptr(weights), ptr(lens), B, S, H, H_kv,
+          D, S_max, w_stride, window, scale, stream_handle(stream))
+
+
+def kv8_evict(src, dst, weights_in, weights_out, seqlens_in, seqlens_out, kept, keep, recent,
+              stream=None):
+    _call("flashsvd_kv8_evict", _kv8(src), _kv8(dst), ptr(weights_in), ptr(weights_out),
+          ptr(seqlens_in), ptr(seqlens_out), ptr(kept), keep, recent, stream_handle(stream))
 
 
 def rmsnorm(x, g, y, M, d, eps, stream=None):
