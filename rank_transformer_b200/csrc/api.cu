@@ -1042,8 +1042,10 @@ int flashsvd_kv8_decode_attn(const flashsvd_bf16* q, const flashsvd_bf16* k_new,
   a.out = (bf16*)out;
   a.H = H;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.part = cur().apart; a.part_cap = (long long)cur().apart_elems;
+  a.part = cur().df_part; a.part_cap = kFusedPartFloats;
+  a.scores = cur().apart; a.scores_cap = (long long)cur().apart_elems;
   a.counters = cur().acounters; a.counters_cap = kCountersN;
+  a.status = cur().status;
   return kv8_attn_launch(a, cur().sm_count, stream);
 }
 

@@ -166,6 +166,9 @@ int decode_plan_launch(const DecodePlan* plan, bf16* x, const int* seqlens, bf16
 void decode_plan_destroy(DecodePlan* plan);
 int encode_map(CUtensorMap* map, const void* base, long long rows, long long cols, long long ld,
                int box_cols, int box_rows, bool swizzle128);
+// Tensor map over `rows` rows of 128 bytes (128-byte swizzle, boxes of
+// box_rows whole rows).
+int encode_map_bytes(CUtensorMap* map, const void* base, long long rows, int box_rows);
 constexpr int kFusedPartFloats = 2 * 148 * 16 * 640;
 // Test hook (flashsvd_debug_drop_barrier_arrival): when set, the next fused
 // decode launch takes it (resetting it) and its CTA 0 skips its first
@@ -212,8 +215,10 @@ struct Kv8AttnParams {
   bf16* out;
   int H;
   float scale_log2;                // scale * log2(e)
-  float* part; long long part_cap; // workspace (floats)
+  float* part; long long part_cap; // workspace (floats): partials, (M, 1 / l) of the heads
+  float* scores; long long scores_cap;  // workspace (floats): scores, when weights are wanted
   int* counters; int counters_cap; // zero between launches
+  int* status;
 };
 constexpr int KV8_MAX_BATCH = 1024;  // batch entries of one attention call
 int kv8_attn_launch(const Kv8AttnParams& p, int sm_count, cudaStream_t stream);

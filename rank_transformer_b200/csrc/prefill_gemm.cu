@@ -64,6 +64,20 @@ int encode_map(CUtensorMap* map, const void* base, long long rows, long long col
   return r == CUDA_SUCCESS ? FLASHSVD_OK : FLASHSVD_ERR_INVALID_ARG;
 }
 
+int encode_map_bytes(CUtensorMap* map, const void* base, long long rows, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return FLASHSVD_ERR_CUDA;
+  if (!aligned16(base)) return FLASHSVD_ERR_MISALIGNED;
+  cuuint64_t dims[2] = {128, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {128};
+  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  cuuint32_t es[2] = {1u, 1u};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FLASHSVD_OK : FLASHSVD_ERR_INVALID_ARG;
+}
+
 namespace {
 
 constexpr int BM = 128;
