@@ -1096,7 +1096,7 @@ int flashsvd_kv8_evict(const flashsvd_kv8* src, const flashsvd_kv8* dst, const f
   a.keep = keep; a.recent = recent; a.in_place = same == 7;
   a.ws = reinterpret_cast<int*>(cur().apart); a.ws_cap = (long long)cur().apart_elems;
   a.status = cur().status;
-  return kv8_evict_launch(a, stream);
+  return kv8_evict_launch(a, cur().sm_count, stream);
 }
 
 int flashsvd_rmsnorm(const flashsvd_bf16* x, const flashsvd_bf16* g,

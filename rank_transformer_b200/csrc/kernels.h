@@ -233,7 +233,7 @@ struct Kv8EvictParams {
   int* ws; long long ws_cap;       // workspace (ints)
   int* status;
 };
-int kv8_evict_launch(const Kv8EvictParams& p, cudaStream_t stream);
+int kv8_evict_launch(const Kv8EvictParams& p, int sm_count, cudaStream_t stream);
 
 // ------------------------------------------- attention weight per key ------
 struct AttnSumsParams {

@@ -3,8 +3,9 @@
 // Launch 1 (select): per (batch row, KV head) with n > keep tokens, the
 // keep - recent largest weights of the first n - recent tokens (ties to the
 // lower index) by a radix selection on the weights' ordered bit patterns,
-// then the kept indices in ascending order.  Launch 2 (move): one CTA per
-// kept 64-token block gathers its rows into registers, finds their new
+// and the kept indices in ascending order.  The weights are read once, into
+// shared memory; long rows are cut over a cluster.  Launch 2 (move): one CTA
+// per kept 64-token block gathers its rows into registers, finds their new
 // scale and writes codes, scale, weights and, for the newest block, the tail.
 //
 // In place, a kept row moves to a lower or equal index, so a CTA may write
@@ -22,7 +23,12 @@ namespace fsvd {
 namespace {
 
 constexpr int EV_SEL_THREADS = 1024;
+constexpr int EV_SEL_STRETCH = 8192;  // weights per CTA of a selection,
+constexpr int EV_SEL_CTAS = 8;        // up to so many CTAs a pair
+constexpr int EV_BINS = 2048;
+constexpr int EV_SEL_KEYS = 24576;   // keys of a stretch held in shared memory (96 KB)
 constexpr int EV_THREADS = 256;
+constexpr int EV_CTAS = 4;              // CTAs per SM (64 registers a thread)
 
 struct EvParams {
   Kv8 src, dst;
@@ -30,6 +36,7 @@ struct EvParams {
   const int* n_in; int* n_out;
   int* kept;
   int keep, recent, in_place, nblk;  // nblk: blocks of `keep` tokens
+  int sel_ctas;                      // CTAs per pair of the selection
   int* n_ws;                         // [B * G] token counts before eviction
   int* flags;                        // [B * G * nblk] rows loaded
   int* ticket;
@@ -44,187 +51,264 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// Exclusive sum over the threads of a block of 1024 (by thread index, or from
+// the last thread down); s: 32 words of shared memory.
+template <bool FROM_TOP>
+__device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s, int lane, int warp) {
+  uint32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = FROM_TOP ? __shfl_down_sync(0xffffffffu, x, o) : __shfl_up_sync(0xffffffffu, x, o);
+    if (FROM_TOP ? lane + o < 32 : lane >= o) x += y;
+  }
+  if (lane == (FROM_TOP ? 0 : 31)) s[warp] = x;
+  __syncthreads();
+  uint32_t w = s[lane];
+  w = __reduce_add_sync(0xffffffffu, (FROM_TOP ? lane > warp : lane < warp) ? w : 0u);
+  return w + x - v;
+}
+
+__device__ __forceinline__ uint2 ld_cluster2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// A cluster of `ctas` CTAs per pair, each with one stretch of the weights.
+// Three passes over 11, 11 and 10 bits of the keys narrow down the hk-th
+// largest key: every CTA counts its stretch's digits, and adds up the counts
+// of all of them through distributed shared memory.  Then the kept indices
+// are written in order: counts per warp, per CTA, and their sums before it.
 __global__ void __launch_bounds__(EV_SEL_THREADS)
 kv8_select_kernel(const __grid_constant__ EvParams p) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t s_prefix, s_need;
-  __shared__ uint32_t s_warp[32];
+  extern __shared__ uint32_t keys[];  // [EV_SEL_KEYS] this stretch's keys, if they fit
+  __shared__ __align__(16) uint32_t hist[EV_BINS];
+  __shared__ uint32_t s_scan[32], s_res[2], s_wg[32], s_we[32];
+  __shared__ __align__(8) uint32_t s_tot[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int pair = blockIdx.x, b = pair / p.src.G;
+  const int ctas = p.sel_ctas, rank = blockIdx.x % ctas;
+  const int pair = blockIdx.x / ctas, b = pair / p.src.G;
 
   pdl_launch_dependents();
   pdl_wait();
 
-  for (int i = tid; i < p.nblk; i += EV_SEL_THREADS) p.flags[(long long)pair * p.nblk + i] = 0;
-  if (pair == 0 && tid == 0) *p.ticket = 0;
+  const int t0 = rank * EV_SEL_THREADS + tid, step = ctas * EV_SEL_THREADS;
+  for (int i = t0; i < p.nblk; i += step) p.flags[(long long)pair * p.nblk + i] = 0;
+  if (blockIdx.x == 0 && tid == 0) *p.ticket = 0;
   int n = p.n_in[b];
   n = n < 0 ? 0 : (n > p.src.S_max ? p.src.S_max : n);
-  if (tid == 0) p.n_ws[pair] = n;
+  if (rank == 0 && tid == 0) p.n_ws[pair] = n;
   int* kept = p.kept + (long long)pair * p.keep;
   if (n <= p.keep) {
-    for (int i = tid; i < p.keep; i += EV_SEL_THREADS) kept[i] = i < n ? i : -1;
+    for (int i = t0; i < p.keep; i += step) kept[i] = i < n ? i : -1;
     return;
   }
   const int c = n - p.recent, hk = p.keep - p.recent;
-  for (int i = tid; i < p.recent; i += EV_SEL_THREADS) kept[hk + i] = c + i;
+  for (int i = t0; i < p.recent; i += step) kept[hk + i] = c + i;
   if (hk == 0) return;
-  const float* w = p.w_in + (long long)pair * p.src.S_max;
 
-  // the hk-th largest key: one byte per pass, from the top
+  // this CTA's stretch [first, first + len), a multiple of 1024 long but for the last
+  const int chunk = ((c + ctas - 1) / ctas + EV_SEL_THREADS - 1) / EV_SEL_THREADS * EV_SEL_THREADS;
+  const int first = rank * chunk, len = max(0, min(chunk, c - first));
+  const float* w = p.w_in + (long long)pair * p.src.S_max + first;
+  const bool cached = len <= EV_SEL_KEYS;
+  if (cached)
+    for (int i = tid * 4; i < len; i += 4 * EV_SEL_THREADS) {
+      const float4 v = *reinterpret_cast<const float4*>(w + i);  // (rows are padded to 64)
+      *reinterpret_cast<uint4*>(keys + i) = make_uint4(order_key(v.x), order_key(v.y), order_key(v.z), order_key(v.w));
+    }
+  auto key = [&](int i) { return cached ? keys[i] : order_key(w[i]); };
+
   uint32_t prefix = 0, need = hk;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
+  const uint32_t hist_at = tc::smem_u32(hist);
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    hist[tid] = hist[tid + EV_SEL_THREADS] = 0;
     __syncthreads();
-    for (int i = tid; i < c; i += EV_SEL_THREADS) {
-      const uint32_t k = order_key(w[i]);
-      if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+    for (int i = tid; i < len; i += EV_SEL_THREADS) {
+      const uint32_t k = key(i);
+      if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
     }
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t above = 0;
-      int d = 255;
-      for (; d > 0 && above + hist[d] < need; --d) above += hist[d];
-      s_prefix = (prefix << 8) | (uint32_t)d;
-      s_need = need - above;
-    }
-    __syncthreads();
-    prefix = s_prefix;
-    need = s_need;
-    __syncthreads();
-  }
-  // in order: every key above it, and the first `need` equal to it
-  uint32_t n_gt = 0, n_eq = 0;  // before this stretch
-  for (int i0 = 0; i0 < c; i0 += EV_SEL_THREADS) {
-    const int i = i0 + tid;
-    const uint32_t k = i < c ? order_key(w[i]) : 0u;
-    const bool gt = i < c && k > prefix, eq = i < c && k == prefix;
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) s_warp[warp] = (uint32_t)__popc(bg) | ((uint32_t)__popc(be) << 16);
-    __syncthreads();
-    uint32_t v = s_warp[lane], before = 0, total = 0;
-    uint32_t x = v;
+    if (ctas > 1) tc::cluster_sync(); else __syncthreads();
+    uint32_t c0 = 0, c1 = 0;  // digits 2 tid and 2 tid + 1
+    uint2 cnt[EV_SEL_CTAS];  // (all loads in flight at once: one takes about a microsecond)
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+    for (int r = 0; r < EV_SEL_CTAS; ++r)
+      cnt[r] = r < ctas ? ld_cluster2(tc::mapa_shared(hist_at, r) + 8 * tid) : make_uint2(0, 0);
+#pragma unroll
+    for (int r = 0; r < EV_SEL_CTAS; ++r) { c0 += cnt[r].x; c1 += cnt[r].y; }
+    const uint32_t above = block_before<true>(c0 + c1, s_scan, lane, warp);
+    if (above < need && above + c0 + c1 >= need) {
+      const bool odd = above + c1 >= need;
+      s_res[0] = (prefix << bits) | (uint32_t)(2 * tid + (odd ? 1 : 0));
+      s_res[1] = need - above - (odd ? 0u : c1);
     }
-    total = __shfl_sync(0xffffffffu, x, 31);
-    before = __shfl_sync(0xffffffffu, x - v, warp);
+    if (ctas > 1) tc::cluster_sync(); else __syncthreads();
+    prefix = s_res[0];
+    need = s_res[1];
+  }
+
+  // every key above `prefix`, and the first `need` equal to it
+  const int seg = chunk / 32, s0 = min(len, warp * seg), s1 = min(len, s0 + seg);
+  uint32_t ng = 0, ne = 0;
+  for (int i = s0; i < s1; i += 32) {
+    const uint32_t k = i + lane < s1 ? key(i + lane) : 0u;
+    ng += __popc(__ballot_sync(0xffffffffu, i + lane < s1 && k > prefix));
+    ne += __popc(__ballot_sync(0xffffffffu, i + lane < s1 && k == prefix));
+  }
+  if (lane == 0) { s_wg[warp] = ng; s_we[warp] = ne; }
+  __syncthreads();
+  uint32_t g = __reduce_add_sync(0xffffffffu, lane < warp ? s_wg[lane] : 0u);
+  uint32_t e = __reduce_add_sync(0xffffffffu, lane < warp ? s_we[lane] : 0u);
+  if (ctas > 1) {
+    if (tid == EV_SEL_THREADS - 32) { s_tot[0] = g + ng; s_tot[1] = e + ne; }
+    tc::cluster_sync();
+    const uint2 t = lane < rank ? ld_cluster2(tc::mapa_shared(tc::smem_u32(s_tot), lane)) : make_uint2(0, 0);
+    g += __reduce_add_sync(0xffffffffu, t.x);
+    e += __reduce_add_sync(0xffffffffu, t.y);
+    tc::cluster_sync();  // (no CTA leaves while its counts may be read)
+  }
+  for (int i = s0; i < s1; i += 32) {
+    const uint32_t k = i + lane < s1 ? key(i + lane) : 0u;
+    const bool gt = i + lane < s1 && k > prefix, eq = i + lane < s1 && k == prefix;
+    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
     const uint32_t below = (1u << lane) - 1u;
-    const uint32_t g0 = n_gt + (before & 0xffffu) + __popc(bg & below);
-    const uint32_t e0 = n_eq + (before >> 16) + __popc(be & below);
-    if (gt || (eq && e0 < need)) kept[g0 + min(e0, need)] = i;
-    n_gt += total & 0xffffu;
-    n_eq += total >> 16;
-    __syncthreads();
+    const uint32_t e0 = e + __popc(be & below);
+    if (gt || (eq && e0 < need)) kept[g + __popc(bg & below) + min(e0, need)] = first + i + lane;
+    g += __popc(bg);
+    e += __popc(be);
   }
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(EV_THREADS)
+__global__ void __launch_bounds__(EV_THREADS, EV_CTAS)
 kv8_move_kernel(const __grid_constant__ EvParams p) {
   constexpr int UPR = D / 16;                 // units of 16 elements per row
   constexpr int PER = KV8_BLOCK * UPR / 128;  // units per thread; 128 threads per tensor
   __shared__ int s_idx[KV8_BLOCK];
   __shared__ uint32_t s_max[EV_THREADS / 32];
-  __shared__ int s_item, s_ok;
+  __shared__ int s_next, s_ok;
   const int tid = threadIdx.x, x = tid >> 7, t = tid & 127;
+  const int items = p.src.B * p.src.G * p.nblk;
 
   pdl_launch_dependents();
   pdl_wait();
 
-  if (tid == 0) { s_item = atomicAdd(p.ticket, 1); s_ok = 1; }
+  // Items come from a counter, each CTA one ahead: while an item's rows are
+  // on their way, the next item's number and indices are fetched.
+  if (tid == 0) { s_next = atomicAdd(p.ticket, 1); s_ok = 1; }
   __syncthreads();
-  const int pair = s_item / p.nblk, i = s_item - pair * p.nblk;
-  const int b = pair / p.src.G;
-  const int n = p.n_ws[pair], m = min(n, p.keep);
-  if (i == 0 && pair == b * p.src.G && tid == 0 && p.n_out) p.n_out[b] = m;
-  const bool still = p.in_place && n <= p.keep;  // nothing moves
-  const int row0 = i * KV8_BLOCK, rows = min(KV8_BLOCK, m - row0);
-  if (still || rows <= 0) return;
-  const int* kept = p.kept + (long long)pair * p.keep;
-  if (tid < KV8_BLOCK) s_idx[tid] = tid < rows ? kept[row0 + tid] : -1;
-  __syncthreads();
-
-  // ---- load the rows as bf16 and the weights ----
-  const int last = (n - 1) / KV8_BLOCK;  // the source's newest block: in its tail
-  const uint8_t* codes = p.src.codes[x] + (long long)pair * p.src.S_max * D;
-  const float* scale = p.src.scale[x] + (long long)pair * (p.src.S_max / KV8_BLOCK);
-  const bf16* stail = p.src.tail[x] + (long long)pair * KV8_BLOCK * D;
-  uint4 a[PER], c[PER];
-  uint32_t mx = 0;
-#pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int u = t + 128 * k, r = s_idx[u / UPR], col = (u % UPR) * 16;
-    a[k] = c[k] = make_uint4(0, 0, 0, 0);
-    if (r >= 0) {
-      if (r / KV8_BLOCK == last) {
-        a[k] = ld_once(stail + (r % KV8_BLOCK) * D + col);
-        c[k] = ld_once(stail + (r % KV8_BLOCK) * D + col + 8);
-      } else {
-        kv8_decode16<E4M3>(ld_once(codes + (long long)r * D + col), scale[r / KV8_BLOCK], a[k], c[k]);
-      }
-    }
-  }
-  float wv = 0.f;
-  if (tid < rows) wv = p.w_in[(long long)pair * p.src.S_max + s_idx[tid]];
-#pragma unroll
-  for (int k = 0; k < PER; ++k) mx = max(mx, max(amax8(a[k]), amax8(c[k])));
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  if ((tid & 31) == 0) s_max[tid >> 5] = mx;
-  __syncthreads();
-
-  if (p.in_place) {
-    int* flags = p.flags + (long long)pair * p.nblk;
+  int item = s_next, idx = -1, n = 0;
+  auto fetch = [&]() {
+    if (item >= items) return;
+    const int pair = item / p.nblk, row = (item - pair * p.nblk) * KV8_BLOCK + tid;
+    n = p.n_ws[pair];
+    if (tid < KV8_BLOCK) idx = row < p.keep ? p.kept[(long long)pair * p.keep + row] : -1;
+  };
+  fetch();
+  while (item < items) {
+    const int pair = item / p.nblk, i = item - pair * p.nblk;
+    const int m = min(n, p.keep), row0 = i * KV8_BLOCK, rows = min(KV8_BLOCK, m - row0);
+    const bool moves = rows > 0 && !(p.in_place && n <= p.keep);
+    if (tid < KV8_BLOCK) s_idx[tid] = idx;
+    __syncthreads();  // s_idx written; s_next read by all
     if (tid == 0) {
-      __threadfence();
-      asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(flags + i) : "memory");
+      s_next = atomicAdd(p.ticket, 1);
+      if (i == 0 && pair % p.src.G == 0 && p.n_out) p.n_out[pair / p.src.G] = m;
     }
-    // blocks j < i whose last row lies in block i or beyond (the source's
-    // newest block, whose rows the tail holds, is never below block i)
-    if (tid < 32) {
-      const long long t0 = clock64();
-      for (int j = i - 1 - tid; j >= 0; j -= 32) {
-        if (kept[j * KV8_BLOCK + KV8_BLOCK - 1] < row0) break;
-        int v = 0;
-        while (true) {
-          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flags + j) : "memory");
-          if (v) break;
-          if (clock64() - t0 > tc::kWaitCycles) {
-            atomicExch(p.status, DEV_STATUS_TIMEOUT);
-            s_ok = 0;
-            break;
-          }
-          __nanosleep(32);
+
+    // ---- load the rows as bf16 and the weights ----
+    const int last = (n - 1) / KV8_BLOCK;  // the source's newest block: in its tail
+    uint4 a[PER], c[PER];
+    float wv = 0.f;
+    if (moves) {
+      const uint8_t* codes = p.src.codes[x] + (long long)pair * p.src.S_max * D;
+      const float* scale = p.src.scale[x] + (long long)pair * (p.src.S_max / KV8_BLOCK);
+      const bf16* stail = p.src.tail[x] + (long long)pair * KV8_BLOCK * D;
+      float sc[PER];
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int u = t + 128 * k, r = s_idx[u / UPR], col = (u % UPR) * 16;
+        a[k] = c[k] = make_uint4(0, 0, 0, 0);
+        sc[k] = -1.f;  // bf16 already
+        if (r >= 0 && r / KV8_BLOCK == last) {
+          a[k] = ld_once(stail + (r % KV8_BLOCK) * D + col);
+          c[k] = ld_once(stail + (r % KV8_BLOCK) * D + col + 8);
+        } else if (r >= 0) {
+          a[k] = ld_once(codes + (long long)r * D + col);
+          sc[k] = scale[r / KV8_BLOCK];
         }
-        if (!v) break;
       }
-      __threadfence();
+      if (tid < rows) wv = p.w_in[(long long)pair * p.src.S_max + s_idx[tid]];
+      uint32_t mx = 0;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        if (!(sc[k] < 0.f)) kv8_decode16<E4M3>(a[k], sc[k], a[k], c[k]);  // (a NaN scale too)
+        mx = max(mx, max(amax8(a[k]), amax8(c[k])));
+      }
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      if ((tid & 31) == 0) s_max[tid >> 5] = mx;
     }
     __syncthreads();
-    if (!s_ok) return;
-  }
+    item = s_next;
+    const int n_cur = n;
+    fetch();
+    if (!moves) continue;
 
-  // ---- write ----
-  if (tid < rows) p.w_out[(long long)pair * p.dst.S_max + row0 + tid] = wv;
-  if (rows == KV8_BLOCK) {
-    mx = max(max(s_max[4 * x], s_max[4 * x + 1]), max(s_max[4 * x + 2], s_max[4 * x + 3]));
-    const int e = kv8_exponent<E4M3>(mx);
-    const bool fin = kv8_finite(mx);
-    uint8_t* dst = p.dst.codes[x] + ((long long)pair * p.dst.S_max + row0) * D;
+    if (p.in_place) {
+      int* flags = p.flags + (long long)pair * p.nblk;
+      const int* kept = p.kept + (long long)pair * p.keep;
+      if (tid == 0) {
+        __threadfence();
+        asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(flags + i) : "memory");
+      }
+      // blocks j < i whose last row lies in block i or beyond (the source's
+      // newest block, whose rows the tail holds, is never below block i)
+      if (tid < 32) {
+        const long long t0 = clock64();
+        for (int j = i - 1 - tid; j >= 0; j -= 32) {
+          if (kept[j * KV8_BLOCK + KV8_BLOCK - 1] < row0) break;
+          int v = 0;
+          while (true) {
+            asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(flags + j) : "memory");
+            if (v) break;
+            if (clock64() - t0 > tc::kWaitCycles) {
+              atomicExch(p.status, DEV_STATUS_TIMEOUT);
+              s_ok = 0;
+              break;
+            }
+            __nanosleep(32);
+          }
+          if (!v) break;
+        }
+        __threadfence();
+      }
+      __syncthreads();
+      if (!s_ok) return;
+    }
+
+    // ---- write ----
+    if (tid < rows) p.w_out[(long long)pair * p.dst.S_max + row0 + tid] = wv;
+    if (rows == KV8_BLOCK) {
+      const uint32_t mx = max(max(s_max[4 * x], s_max[4 * x + 1]), max(s_max[4 * x + 2], s_max[4 * x + 3]));
+      const int e = kv8_exponent<E4M3>(mx);
+      const bool fin = kv8_finite(mx);
+      uint8_t* dst = p.dst.codes[x] + ((long long)pair * p.dst.S_max + row0) * D;
 #pragma unroll
-    for (int k = 0; k < PER; ++k)
-      *reinterpret_cast<uint4*>(dst + (t + 128 * k) * 16) = kv8_encode16<E4M3>(a[k], c[k], exp2i(-e), fin);
-    if (t == 0) p.dst.scale[x][(long long)pair * (p.dst.S_max / KV8_BLOCK) + i] = kv8_scale(e, fin);
-  }
-  if (row0 + KV8_BLOCK >= m) {
-    bf16* tail = p.dst.tail[x] + (long long)pair * KV8_BLOCK * D;
+      for (int k = 0; k < PER; ++k)
+        *reinterpret_cast<uint4*>(dst + (t + 128 * k) * 16) = kv8_encode16<E4M3>(a[k], c[k], exp2i(-e), fin);
+      if (t == 0) p.dst.scale[x][(long long)pair * (p.dst.S_max / KV8_BLOCK) + i] = kv8_scale(e, fin);
+    }
+    if (row0 + KV8_BLOCK >= min(n_cur, p.keep)) {
+      bf16* tail = p.dst.tail[x] + (long long)pair * KV8_BLOCK * D;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int u = t + 128 * k;
-      if (u / UPR < rows) {
-        *reinterpret_cast<uint4*>(tail + u * 16) = a[k];
-        *reinterpret_cast<uint4*>(tail + u * 16 + 8) = c[k];
+      for (int k = 0; k < PER; ++k) {
+        const int u = t + 128 * k;
+        if (u / UPR < rows) {
+          *reinterpret_cast<uint4*>(tail + u * 16) = a[k];
+          *reinterpret_cast<uint4*>(tail + u * 16 + 8) = c[k];
+        }
       }
     }
   }
@@ -232,7 +316,7 @@ kv8_move_kernel(const __grid_constant__ EvParams p) {
 
 }  // namespace
 
-int kv8_evict_launch(const Kv8EvictParams& a, cudaStream_t stream) {
+int kv8_evict_launch(const Kv8EvictParams& a, int sm_count, cudaStream_t stream) {
   EvParams p;
   memset(&p, 0, sizeof(p));
   p.src = a.src; p.dst = a.dst;
@@ -248,9 +332,17 @@ int kv8_evict_launch(const Kv8EvictParams& a, cudaStream_t stream) {
   p.n_ws = a.ws + 4;
   p.flags = p.n_ws + pairs;
   const LaunchTag st{"kv8_select", 4.0 * pairs * ((double)a.src.S_max + a.keep), 0.0};
-  FSVD_TRY(launch_pdl(st, kv8_select_kernel, dim3((unsigned)pairs), dim3(EV_SEL_THREADS), 0, stream, p));
+  p.sel_ctas = 1;
+  while (p.sel_ctas < EV_SEL_CTAS && p.sel_ctas * EV_SEL_STRETCH < a.src.S_max) p.sel_ctas *= 2;
+  const int stretch = round_up(ceil_div(a.src.S_max, p.sel_ctas), EV_SEL_THREADS);
+  const size_t smem = 4 * (size_t)(stretch < EV_SEL_KEYS ? stretch : EV_SEL_KEYS);
+  static SmemAttrOnce once;
+  FSVD_TRY(set_smem_once(once, kv8_select_kernel, EV_SEL_KEYS * 4));
+  FSVD_TRY(launch_pdl_cluster(st, p.sel_ctas, kv8_select_kernel, dim3((unsigned)(pairs * p.sel_ctas)), dim3(EV_SEL_THREADS),
+                              smem, stream, p));
   const LaunchTag mt{"kv8_move", pairs * (double)a.keep * (4.0 * a.src.D + 12.0), 0.0};
-  const dim3 grid((unsigned)items), block(EV_THREADS);
+  const long long most = (long long)sm_count * EV_CTAS;
+  const dim3 grid((unsigned)(items < most ? items : most)), block(EV_THREADS);
   if (a.src.D == 128)
     return a.src.e4m3 ? launch_pdl(mt, kv8_move_kernel<128, true>, grid, block, 0, stream, p)
                       : launch_pdl(mt, kv8_move_kernel<128, false>, grid, block, 0, stream, p);
