@@ -112,6 +112,48 @@ __device__ __forceinline__ void kv8_decode4(uint32_t w, uint32_t& lo, uint32_t& 
     hi = *reinterpret_cast<uint32_t*>(&y);
   }
 }
+// Sixteen codes -> eight half pairs (in order, exact).
+template <bool E4M3>
+__device__ __forceinline__ void kv8_decode16h(const uint4& c, __half2* h) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t lo, hi;
+    kv8_decode4<E4M3>(w[i], lo, hi);
+    h[2 * i] = *reinterpret_cast<__half2*>(&lo);
+    h[2 * i + 1] = *reinterpret_cast<__half2*>(&hi);
+  }
+}
+// Sixteen codes (as halves) of a block with exponent e + shift -> codes for
+// the exponent e: code * 2^shift rounded to nearest, ties to even; at most
+// the format's limit by the choice of e.  A shift below -20 rounds every code
+// to zero, as -20 does.  In half precision the product is exact wherever the
+// result is not zero, and adding 1.5 * 2^10 in the same instruction rounds it
+// to an integer whose two's complement is the low byte (int8).
+template <bool E4M3>
+__device__ __forceinline__ uint4 kv8_rescale16(const __half2* h, int shift) {
+  // (a shift above 14 occurs only with zero codes: a code of 1 or 2^-9 would
+  // pass the limit at 7 or 18, so e4m3 goes in two steps)
+  shift = shift < -20 ? -20 : (shift > 24 ? 24 : shift);
+  const int s1 = shift / 2, s2 = shift - s1;
+  const __half2 f1 = __float2half2_rn(exp2i(s1)), f2 = __float2half2_rn(exp2i(s2));
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (E4M3) {
+      const __half2 x = __hmul2(__hmul2(h[2 * i], f1), f2), y = __hmul2(__hmul2(h[2 * i + 1], f1), f2);
+      uint16_t lo, hi;
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(*reinterpret_cast<const uint32_t*>(&y)));
+      r[i] = (uint32_t)lo | ((uint32_t)hi << 16);
+    } else {
+      const __half2 c = __float2half2_rn(1536.f);
+      const __half2 x = __hfma2(__hmul2(h[2 * i], f1), f2, c), y = __hfma2(__hmul2(h[2 * i + 1], f1), f2, c);
+      r[i] = __byte_perm(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y), 0x6420);
+    }
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
 // Sixteen codes times the scale -> sixteen bf16 (exact).
 template <bool E4M3>
 __device__ __forceinline__ void kv8_decode16(const uint4& c, float s, uint4& a, uint4& b) {

@@ -22,11 +22,10 @@
 namespace fsvd {
 namespace {
 
-constexpr int EV_SEL_THREADS = 1024;
-constexpr int EV_SEL_STRETCH = 8192;  // weights per CTA of a selection,
+constexpr int EV_SEL_THREADS = 512;
+constexpr int EV_SEL_STRETCH = 4096;  // weights per CTA of a selection,
 constexpr int EV_SEL_CTAS = 8;        // up to so many CTAs a pair
 constexpr int EV_BINS = 2048;
-constexpr int EV_SEL_KEYS = 24576;   // keys of a stretch held in shared memory (96 KB)
 constexpr int EV_THREADS = 256;
 constexpr int EV_CTAS = 4;              // CTAs per SM (64 registers a thread)
 
@@ -51,10 +50,11 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive sum over the threads of a block of 1024 (by thread index, or from
-// the last thread down); s: 32 words of shared memory.
+// Exclusive sum over the threads of the block (by thread index, or from the
+// last thread down) and the sum of all; s: one word a warp of shared memory.
 template <bool FROM_TOP>
-__device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s, int lane, int warp) {
+__device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s, int lane, int warp, uint32_t* total) {
+  constexpr int WARPS = EV_SEL_THREADS / 32;
   uint32_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -63,9 +63,9 @@ __device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s, int la
   }
   if (lane == (FROM_TOP ? 0 : 31)) s[warp] = x;
   __syncthreads();
-  uint32_t w = s[lane];
-  w = __reduce_add_sync(0xffffffffu, (FROM_TOP ? lane > warp : lane < warp) ? w : 0u);
-  return w + x - v;
+  const uint32_t w = lane < WARPS ? s[lane] : 0u;
+  *total = __reduce_add_sync(0xffffffffu, w);
+  return __reduce_add_sync(0xffffffffu, (FROM_TOP ? lane > warp : lane < warp) ? w : 0u) + x - v;
 }
 
 __device__ __forceinline__ uint2 ld_cluster2(uint32_t addr) {
@@ -73,17 +73,29 @@ __device__ __forceinline__ uint2 ld_cluster2(uint32_t addr) {
   asm volatile("ld.shared::cluster.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ uint4 ld_cluster4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 
-// A cluster of `ctas` CTAs per pair, each with one stretch of the weights.
-// Three passes over 11, 11 and 10 bits of the keys narrow down the hk-th
-// largest key: every CTA counts its stretch's digits, and adds up the counts
-// of all of them through distributed shared memory.  Then the kept indices
-// are written in order: counts per warp, per CTA, and their sums before it.
-__global__ void __launch_bounds__(EV_SEL_THREADS)
+// A cluster of `ctas` CTAs per pair, each with one stretch of the weights;
+// every thread keeps KPT consecutive ones in registers (a stretch longer than
+// a CTA's threads hold is walked in tiles, read again each time).  Three
+// passes over 11, 11 and 10 bits of the keys narrow down the hk-th largest
+// key: every CTA counts its stretch's digits, and adds up the counts of all
+// of them through distributed shared memory.  Then the kept indices are
+// written in order, at the sum of the counts before them.
+template <int KPT>
+__global__ void __launch_bounds__(EV_SEL_THREADS, 2)
 kv8_select_kernel(const __grid_constant__ EvParams p) {
-  extern __shared__ uint32_t keys[];  // [EV_SEL_KEYS] this stretch's keys, if they fit
+  constexpr int TILE = EV_SEL_THREADS * KPT, BPT = EV_BINS / EV_SEL_THREADS;
+  static_assert(BPT == 4, "four digits a thread");
   __shared__ __align__(16) uint32_t hist[EV_BINS];
-  __shared__ uint32_t s_scan[32], s_res[2], s_wg[32], s_we[32];
+  __shared__ uint32_t s_scan[EV_SEL_THREADS / 32], s_res[2];
   __shared__ __align__(8) uint32_t s_tot[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = p.sel_ctas, rank = blockIdx.x % ctas;
@@ -107,42 +119,62 @@ kv8_select_kernel(const __grid_constant__ EvParams p) {
   for (int i = t0; i < p.recent; i += step) kept[hk + i] = c + i;
   if (hk == 0) return;
 
-  // this CTA's stretch [first, first + len), a multiple of 1024 long but for the last
-  const int chunk = ((c + ctas - 1) / ctas + EV_SEL_THREADS - 1) / EV_SEL_THREADS * EV_SEL_THREADS;
+  // this CTA's stretch [first, first + len), a multiple of four long but for the last
+  const int chunk = ((c + ctas - 1) / ctas + 3) & ~3;
   const int first = rank * chunk, len = max(0, min(chunk, c - first));
+  const int tiles = (chunk + TILE - 1) / TILE;
   const float* w = p.w_in + (long long)pair * p.src.S_max + first;
-  const bool cached = len <= EV_SEL_KEYS;
-  if (cached)
-    for (int i = tid * 4; i < len; i += 4 * EV_SEL_THREADS) {
-      const float4 v = *reinterpret_cast<const float4*>(w + i);  // (rows are padded to 64)
-      *reinterpret_cast<uint4*>(keys + i) = make_uint4(order_key(v.x), order_key(v.y), order_key(v.z), order_key(v.w));
-    }
-  auto key = [&](int i) { return cached ? keys[i] : order_key(w[i]); };
+  uint32_t keys[KPT];
+  int have = 0;  // keys of this thread
+  auto load = [&](int tile) {
+    const int i0 = tile * TILE + tid * KPT;
+    have = max(0, min(KPT, len - i0));
+#pragma unroll
+    for (int k = 0; k < KPT; k += 4)
+      if (k < have) {  // (rows are padded to 64 weights)
+        const float4 v = *reinterpret_cast<const float4*>(w + i0 + k);
+        keys[k] = order_key(v.x); keys[k + 1] = order_key(v.y);
+        keys[k + 2] = order_key(v.z); keys[k + 3] = order_key(v.w);
+      }
+  };
+  load(0);
 
-  uint32_t prefix = 0, need = hk;
-  const uint32_t hist_at = tc::smem_u32(hist);
+  uint32_t prefix = 0, need = hk, total;
+  const uint32_t hist_at = tc::smem_u32(hist) + 4 * BPT * tid;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    hist[tid] = hist[tid + EV_SEL_THREADS] = 0;
+    *reinterpret_cast<uint4*>(hist + BPT * tid) = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    for (int i = tid; i < len; i += EV_SEL_THREADS) {
-      const uint32_t k = key(i);
-      if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+    for (int tile = 0; tile < tiles; ++tile) {
+      if (tiles > 1) load(tile);
+#pragma unroll
+      for (int k = 0; k < KPT; ++k)
+        if (k < have && (pass == 0 || (keys[k] >> (shift + bits)) == prefix))
+          atomicAdd(&hist[(keys[k] >> shift) & ((1u << bits) - 1u)], 1u);
     }
     if (ctas > 1) tc::cluster_sync(); else __syncthreads();
-    uint32_t c0 = 0, c1 = 0;  // digits 2 tid and 2 tid + 1
-    uint2 cnt[EV_SEL_CTAS];  // (all loads in flight at once: one takes about a microsecond)
+    uint32_t d[BPT] = {0, 0, 0, 0};  // counts of digits 4 tid .. + 3
 #pragma unroll
-    for (int r = 0; r < EV_SEL_CTAS; ++r)
-      cnt[r] = r < ctas ? ld_cluster2(tc::mapa_shared(hist_at, r) + 8 * tid) : make_uint2(0, 0);
+    for (int r0 = 0; r0 < EV_SEL_CTAS; r0 += 4) {
+      uint4 v[4];  // (loads in flight together: one takes about a microsecond)
 #pragma unroll
-    for (int r = 0; r < EV_SEL_CTAS; ++r) { c0 += cnt[r].x; c1 += cnt[r].y; }
-    const uint32_t above = block_before<true>(c0 + c1, s_scan, lane, warp);
-    if (above < need && above + c0 + c1 >= need) {
-      const bool odd = above + c1 >= need;
-      s_res[0] = (prefix << bits) | (uint32_t)(2 * tid + (odd ? 1 : 0));
-      s_res[1] = need - above - (odd ? 0u : c1);
+      for (int r = 0; r < 4; ++r)
+        v[r] = r0 + r < ctas ? ld_cluster4(tc::mapa_shared(hist_at, r0 + r)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) { d[0] += v[r].x; d[1] += v[r].y; d[2] += v[r].z; d[3] += v[r].w; }
+    }
+    const uint32_t sum = d[0] + d[1] + d[2] + d[3];
+    uint32_t above = block_before<true>(sum, s_scan, lane, warp, &total);
+    if (above < need && above + sum >= need) {
+#pragma unroll
+      for (int k = BPT - 1; k >= 0; --k) {
+        if (above < need && above + d[k] >= need) {
+          s_res[0] = (prefix << bits) | (uint32_t)(BPT * tid + k);
+          s_res[1] = need - above;
+        }
+        above += d[k];
+      }
     }
     if (ctas > 1) tc::cluster_sync(); else __syncthreads();
     prefix = s_res[0];
@@ -150,34 +182,47 @@ kv8_select_kernel(const __grid_constant__ EvParams p) {
   }
 
   // every key above `prefix`, and the first `need` equal to it
-  const int seg = chunk / 32, s0 = min(len, warp * seg), s1 = min(len, s0 + seg);
-  uint32_t ng = 0, ne = 0;
-  for (int i = s0; i < s1; i += 32) {
-    const uint32_t k = i + lane < s1 ? key(i + lane) : 0u;
-    ng += __popc(__ballot_sync(0xffffffffu, i + lane < s1 && k > prefix));
-    ne += __popc(__ballot_sync(0xffffffffu, i + lane < s1 && k == prefix));
-  }
-  if (lane == 0) { s_wg[warp] = ng; s_we[warp] = ne; }
-  __syncthreads();
-  uint32_t g = __reduce_add_sync(0xffffffffu, lane < warp ? s_wg[lane] : 0u);
-  uint32_t e = __reduce_add_sync(0xffffffffu, lane < warp ? s_we[lane] : 0u);
+  uint32_t g = 0, e = 0;  // of those, in the stretches and tiles before
   if (ctas > 1) {
-    if (tid == EV_SEL_THREADS - 32) { s_tot[0] = g + ng; s_tot[1] = e + ne; }
+    uint32_t mine = 0;
+    uint32_t tg = 0, te = 0;
+    for (int tile = 0; tile < tiles; ++tile) {
+      if (tiles > 1) load(tile);
+#pragma unroll
+      for (int k = 0; k < KPT; ++k)
+        if (k < have) mine += keys[k] > prefix ? 1u : keys[k] == prefix ? 0x10000u : 0u;
+      block_before<false>(mine, s_scan, lane, warp, &total);  // (a tile holds under 2^16 keys)
+      __syncthreads();
+      tg += total & 0xffffu; te += total >> 16;
+      mine = 0;
+    }
+    if (tid == 0) { s_tot[0] = tg; s_tot[1] = te; }
     tc::cluster_sync();
     const uint2 t = lane < rank ? ld_cluster2(tc::mapa_shared(tc::smem_u32(s_tot), lane)) : make_uint2(0, 0);
-    g += __reduce_add_sync(0xffffffffu, t.x);
-    e += __reduce_add_sync(0xffffffffu, t.y);
+    g = __reduce_add_sync(0xffffffffu, t.x);
+    e = __reduce_add_sync(0xffffffffu, t.y);
     tc::cluster_sync();  // (no CTA leaves while its counts may be read)
   }
-  for (int i = s0; i < s1; i += 32) {
-    const uint32_t k = i + lane < s1 ? key(i + lane) : 0u;
-    const bool gt = i + lane < s1 && k > prefix, eq = i + lane < s1 && k == prefix;
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t e0 = e + __popc(be & below);
-    if (gt || (eq && e0 < need)) kept[g + __popc(bg & below) + min(e0, need)] = first + i + lane;
-    g += __popc(bg);
-    e += __popc(be);
+  for (int tile = 0; tile < tiles; ++tile) {
+    if (tiles > 1) load(tile);
+    uint32_t mine = 0;
+#pragma unroll
+    for (int k = 0; k < KPT; ++k)
+      if (k < have) mine += keys[k] > prefix ? 1u : keys[k] == prefix ? 0x10000u : 0u;
+    const uint32_t before = block_before<false>(mine, s_scan, lane, warp, &total);
+    uint32_t gk = g + (before & 0xffffu), ek = e + (before >> 16);
+    const int at = first + tile * TILE + tid * KPT;
+#pragma unroll
+    for (int k = 0; k < KPT; ++k)
+      if (k < have) {
+        const bool gt = keys[k] > prefix, eq = keys[k] == prefix;
+        if (gt || (eq && ek < need)) kept[gk + min(ek, need)] = at + k;
+        gk += gt;
+        ek += eq;
+      }
+    g += total & 0xffffu;
+    e += total >> 16;
+    __syncthreads();
   }
 }
 
@@ -218,15 +263,22 @@ kv8_move_kernel(const __grid_constant__ EvParams p) {
       if (i == 0 && pair % p.src.G == 0 && p.n_out) p.n_out[pair / p.src.G] = m;
     }
 
-    // ---- load the rows as bf16 and the weights ----
+    // ---- load the rows and the weights ----
+    // `codes_only`: every row comes from codes and goes to codes.  The rows
+    // then stay half-precision codes: the new code is the old one times a
+    // power of two, rounded, in one or two instructions a pair.  Otherwise
+    // (the source's newest block, which is in its tail, or the destination's)
+    // they become bf16.  (All of them as bf16 took 12 instructions an element
+    // and bound the kernel: 132 us, now 111, for 32 x 32768 rows of 128.)
     const int last = (n - 1) / KV8_BLOCK;  // the source's newest block: in its tail
+    const bool codes_only = row0 + KV8_BLOCK < m && s_idx[KV8_BLOCK - 1] / KV8_BLOCK < last;
     uint4 a[PER], c[PER];
+    float sc[PER];
     float wv = 0.f;
     if (moves) {
       const uint8_t* codes = p.src.codes[x] + (long long)pair * p.src.S_max * D;
       const float* scale = p.src.scale[x] + (long long)pair * (p.src.S_max / KV8_BLOCK);
       const bf16* stail = p.src.tail[x] + (long long)pair * KV8_BLOCK * D;
-      float sc[PER];
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
         const int u = t + 128 * k, r = s_idx[u / UPR], col = (u % UPR) * 16;
@@ -244,8 +296,20 @@ kv8_move_kernel(const __grid_constant__ EvParams p) {
       uint32_t mx = 0;
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        if (!(sc[k] < 0.f)) kv8_decode16<E4M3>(a[k], sc[k], a[k], c[k]);  // (a NaN scale too)
-        mx = max(mx, max(amax8(a[k]), amax8(c[k])));
+        if (codes_only) {
+          __half2 h[8], most;
+          kv8_decode16h<E4M3>(a[k], h);
+          most = __habs2(h[0]);
+#pragma unroll
+          for (int i = 1; i < 8; ++i) most = __hmax2(most, __habs2(h[i]));
+          const float top = fmaxf(__low2float(most), __high2float(most)) * sc[k];  // exact; NaN stays
+          mx = max(mx, __float_as_uint(top) >> 16);
+          memcpy(&a[k], h, 16);
+          memcpy(&c[k], h + 4, 16);
+        } else {
+          if (!(sc[k] < 0.f)) kv8_decode16<E4M3>(a[k], sc[k], a[k], c[k]);  // (a NaN scale too)
+          mx = max(mx, max(amax8(a[k]), amax8(c[k])));
+        }
       }
       mx = __reduce_max_sync(0xffffffffu, mx);
       if ((tid & 31) == 0) s_max[tid >> 5] = mx;
@@ -296,8 +360,18 @@ kv8_move_kernel(const __grid_constant__ EvParams p) {
       const bool fin = kv8_finite(mx);
       uint8_t* dst = p.dst.codes[x] + ((long long)pair * p.dst.S_max + row0) * D;
 #pragma unroll
-      for (int k = 0; k < PER; ++k)
-        *reinterpret_cast<uint4*>(dst + (t + 128 * k) * 16) = kv8_encode16<E4M3>(a[k], c[k], exp2i(-e), fin);
+      for (int k = 0; k < PER; ++k) {
+        uint4 o;
+        if (codes_only) {
+          __half2 h[8];
+          memcpy(h, &a[k], 16);
+          memcpy(h + 4, &c[k], 16);
+          o = fin ? kv8_rescale16<E4M3>(h, (int)(__float_as_uint(sc[k]) >> 23) - 127 - e) : make_uint4(0, 0, 0, 0);
+        } else {
+          o = kv8_encode16<E4M3>(a[k], c[k], exp2i(-e), fin);
+        }
+        *reinterpret_cast<uint4*>(dst + (t + 128 * k) * 16) = o;
+      }
       if (t == 0) p.dst.scale[x][(long long)pair * (p.dst.S_max / KV8_BLOCK) + i] = kv8_scale(e, fin);
     }
     if (row0 + KV8_BLOCK >= min(n_cur, p.keep)) {
@@ -334,12 +408,10 @@ int kv8_evict_launch(const Kv8EvictParams& a, int sm_count, cudaStream_t stream)
   const LaunchTag st{"kv8_select", 4.0 * pairs * ((double)a.src.S_max + a.keep), 0.0};
   p.sel_ctas = 1;
   while (p.sel_ctas < EV_SEL_CTAS && p.sel_ctas * EV_SEL_STRETCH < a.src.S_max) p.sel_ctas *= 2;
-  const int stretch = round_up(ceil_div(a.src.S_max, p.sel_ctas), EV_SEL_THREADS);
-  const size_t smem = 4 * (size_t)(stretch < EV_SEL_KEYS ? stretch : EV_SEL_KEYS);
-  static SmemAttrOnce once;
-  FSVD_TRY(set_smem_once(once, kv8_select_kernel, EV_SEL_KEYS * 4));
-  FSVD_TRY(launch_pdl_cluster(st, p.sel_ctas, kv8_select_kernel, dim3((unsigned)(pairs * p.sel_ctas)), dim3(EV_SEL_THREADS),
-                              smem, stream, p));
+  // eight weights a thread cover the stretch, or (up to 131072 tokens) 32 do
+  const bool small = (long long)p.sel_ctas * EV_SEL_STRETCH >= a.src.S_max;
+  FSVD_TRY(launch_pdl_cluster(st, p.sel_ctas, small ? kv8_select_kernel<8> : kv8_select_kernel<32>,
+                              dim3((unsigned)(pairs * p.sel_ctas)), dim3(EV_SEL_THREADS), 0, stream, p));
   const LaunchTag mt{"kv8_move", pairs * (double)a.keep * (4.0 * a.src.D + 12.0), 0.0};
   const long long most = (long long)sm_count * EV_CTAS;
   const dim3 grid((unsigned)(items < most ? items : most)), block(EV_THREADS);
