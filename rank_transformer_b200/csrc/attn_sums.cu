@@ -39,10 +39,37 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
+// (x0, x1) * (s, s) + (c0, c1) as one packed instruction.
+__device__ __forceinline__ void fma2(float& x0, float& x1, float s, float c0, float c1) {
+  asm("{\n\t.reg .b64 xx, ss, cc;\n\t"
+      "mov.b64 xx, {%0, %1};\n\t"
+      "mov.b64 ss, {%2, %2};\n\t"
+      "mov.b64 cc, {%3, %4};\n\t"
+      "fma.rn.f32x2 xx, xx, ss, cc;\n\t"
+      "mov.b64 {%0, %1}, xx;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(s), "f"(c0), "f"(c1));
+}
+// (a0, a1) += (b0, b1) as one packed instruction.
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 aa, bb;\n\t"
+      "mov.b64 aa, {%0, %1};\n\t"
+      "mov.b64 bb, {%2, %3};\n\t"
+      "add.rn.f32x2 aa, aa, bb;\n\t"
+      "mov.b64 {%0, %1}, aa;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 struct SuParams {
   const int* lens;
   float* weights;
-  float* lse;        // [B][H][runs * 64]; +inf where there is no query
+  float* lse;        // [B][H][runs * 64]: -lse; -inf where there is no query
   float2* part;      // key splits: [B][G][row tiles][splits][128] (max, sum)
   int* counters;     // [B * G * row tiles], zero between launches
   int B, S, H, G, S_max, w_stride, window;
@@ -52,24 +79,129 @@ struct SuParams {
   int* status;
 };
 
+// One kernel's CTA: a tile of 128 rows (queries or keys) is the A operand and
+// is moved into tensor memory once; runs of 64 rows of the other tensor pass
+// through a ring of shared memory as B.  (With both operands in shared memory
+// each 128 x 64 x 16 step reads 6 KB for 32 cycles of products, at 128 bytes a
+// clock: two CTAs on an SM measured 800 cycles a tile instead of 256.)
 template <int D>
 struct SuLayout {
   static constexpr int KB = D / 64;
   static constexpr int RUN_B = SU_RUN * 128;    // one [64 x 64] bf16 block, 8 KB
-  static constexpr int KEY_B = SU_KEYS * 128;   // one [128 x 64] bf16 block, 16 KB
-  // stats: the row tile, then a ring of key tiles
-  static constexpr int KST = 2;
-  static constexpr int ST_K = KB * KEY_B;
-  static constexpr int ST_BAR = ST_K + KST * KB * KEY_B;
-  // sums: the key tile, then a ring of runs and their lse
-  static constexpr int QST = 4;
-  static constexpr int SM_Q = KB * KEY_B;
-  static constexpr int SM_LSE = SM_Q + QST * KB * RUN_B;
-  static constexpr int SM_BAR = SM_LSE + QST * SU_RUN * 4;
-  static constexpr int X_BYTES = 2 * 128 * 8;   // exchange between the two threads of a row
-  static constexpr int ST_SMEM = 1024 + ST_BAR + 256 + X_BYTES;
-  static constexpr int SM_SMEM = 1024 + SM_BAR + 256 + X_BYTES;
+  static constexpr int ROWS_B = 128 * 128;      // one [128 x 64] bf16 block, 16 KB
+  static constexpr int NST = 4;
+  static constexpr int RING = KB * ROWS_B;
+  static constexpr int LSE = RING + NST * KB * RUN_B;      // the runs' -lse (sums)
+  static constexpr int BAR = LSE + NST * SU_RUN * 4;
+  static constexpr int XCH = BAR + 256;                    // exchange between the two threads of a row
+  static constexpr int SMEM = 1024 + XCH + 128 * 8;
+  static constexpr uint32_t TM_S = 64;          // tensor memory: A in [0, D / 2), S buffers of 64 from here
+  static constexpr int NS = 3;
 };
+
+// Barriers of a CTA, in shared memory.
+template <int D>
+struct SuBars {
+  uint64_t a_full, a_tmem, full[SuLayout<D>::NST], empty[SuLayout<D>::NST];
+  uint64_t s_full[SuLayout<D>::NS], s_empty[SuLayout<D>::NS], drain;
+  uint32_t tmem;
+  int abort_flag, last;
+};
+
+// Barrier set-up and tensor memory (held before dependents may start: a
+// dependent kernel that took it first would wait for this one, and this one
+// for it).  `readers`: arrivals that free a ring stage.
+template <int D>
+__device__ __forceinline__ uint32_t su_begin(SuBars<D>* bars, int readers, int warp) {
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&bars->a_full, 1);
+    tc::mbar_init(&bars->a_tmem, 4);
+    for (int i = 0; i < SuLayout<D>::NST; ++i) { tc::mbar_init(bars->full + i, 1); tc::mbar_init(bars->empty + i, readers); }
+    for (int i = 0; i < SuLayout<D>::NS; ++i) { tc::mbar_init(bars->s_full + i, 1); tc::mbar_init(bars->s_empty + i, 4); }
+    tc::mbar_init(&bars->drain, 1);
+    bars->abort_flag = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&bars->tmem, 256);
+    tc::tmem_relinquish();
+    tc::fence_before_sync();
+  }
+  __syncthreads();
+  tc::fence_after_sync();
+  pdl_launch_dependents();
+  pdl_wait();
+  return bars->tmem;
+}
+template <int D>
+__device__ __forceinline__ void su_end(SuBars<D>* bars, uint32_t tmem, int warp, int lane) {
+  tc::fence_before_sync();
+  __syncthreads();
+  if (bars->abort_flag && warp == 0 && lane == 0) {
+    // let copies still in flight land before shared memory is released
+    const long long c0 = clock64();
+    while (clock64() - c0 < 2000000) {}
+  }
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 256);
+  }
+}
+
+// The MMA warp's lane: `n` products A . run^T (runs through the ring) into the
+// S buffers in turn.
+template <int D>
+__device__ __forceinline__ void su_products(SuBars<D>* bars, uint8_t* smem, uint32_t tmem, int n, int* status) {
+  using L = SuLayout<D>;
+  constexpr uint32_t IDESC = tc::idesc_bf16(SU_RUN, false);
+  volatile int* abort_flag = &bars->abort_flag;
+  bool ok = tc::mbar_wait(&bars->a_tmem, 0, abort_flag, status);
+  int st = 0, sb = 0;
+  uint32_t ph = 0, sph = 0;
+  for (int k = 0; k < n && ok; ++k) {
+    if (!(ok = tc::mbar_wait(bars->full + st, ph, abort_flag, status))) break;
+    if (!(ok = tc::mbar_wait(bars->s_empty + sb, sph ^ 1u, abort_flag, status))) break;
+    tc::fence_after_sync();
+    const uint32_t sq = tc::smem_u32(smem + L::RING + st * L::KB * L::RUN_B);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+      tc::mma_bf16_ts(tmem + L::TM_S + sb * SU_RUN, tmem + kk * 8,
+                      tc::sdesc_sw128(sq + (kk >> 2) * L::RUN_B + (kk & 3) * 32, 16, 1024), IDESC, kk > 0 ? 1u : 0u);
+    tc::mma_commit(bars->s_full + sb);
+    tc::mma_commit(bars->empty + st);
+    if (++st == L::NST) { st = 0; ph ^= 1u; }
+    if (++sb == L::NS) { sb = 0; sph ^= 1u; }
+  }
+  tc::mma_commit(&bars->drain);
+  const long long c0 = clock64();
+  while (!tc::mbar_try_wait(&bars->drain, 0) && clock64() - c0 < tc::kWaitCycles) {}
+}
+
+// Four warps: the A tile from shared memory (128-byte swizzle) into tensor
+// memory, row r in lane r, two bf16 per column.
+template <int D>
+__device__ __forceinline__ bool su_a_to_tmem(SuBars<D>* bars, const uint8_t* smem, uint32_t tmem, int row, int lane,
+                                             int* status) {
+  using L = SuLayout<D>;
+  const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->a_full, 0, &bars->abort_flag, status));
+  if (ok) {
+#pragma unroll
+    for (int kb = 0; kb < L::KB; ++kb) {
+      uint32_t r[32];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const uint4 v = *reinterpret_cast<const uint4*>(smem + kb * L::ROWS_B + row * 128 + ((u ^ (row & 7)) << 4));
+        r[4 * u] = v.x; r[4 * u + 1] = v.y; r[4 * u + 2] = v.z; r[4 * u + 3] = v.w;
+      }
+      tc::tmem_st32(tmem + ((uint32_t)(row & ~31) << 16) + kb * 32, r);
+    }
+    tc::tmem_st_wait();
+  }
+  tc::fence_before_sync();
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(&bars->a_tmem);
+  return ok;
+}
 
 // Sequence geometry of one batch row.
 struct SuRow {
@@ -89,43 +221,14 @@ attn_stats_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   using L = SuLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::ST_BAR);
-  uint64_t* k_full = q_full + 1;           // [KST]
-  uint64_t* k_empty = k_full + L::KST;     // [KST]
-  uint64_t* s_full = k_empty + L::KST;     // [2]
-  uint64_t* s_empty = s_full + 2;          // [2]
-  uint64_t* drain = s_empty + 2;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* s_last = reinterpret_cast<int*>(tmem_holder + 2);
-  float2* xch = reinterpret_cast<float2*>(smem + L::ST_BAR + 256);  // [2][128]
+  SuBars<D>* bars = reinterpret_cast<SuBars<D>*>(smem + L::BAR);
+  float2* xch = reinterpret_cast<float2*>(smem + L::XCH);  // [128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (threadIdx.x == 0) {
-    tc::mbar_init(q_full, 1);
-    for (int i = 0; i < L::KST; ++i) { tc::mbar_init(k_full + i, 1); tc::mbar_init(k_empty + i, 1); }
-    for (int i = 0; i < 2; ++i) { tc::mbar_init(s_full + i, 1); tc::mbar_init(s_empty + i, 8); }
-    tc::mbar_init(drain, 1);
-    *abort_flag = 0;
-    tc::fence_barrier_init();
-  }
-  if (warp == 1) {
-    tc::tmem_alloc(tmem_holder, 256);
-    tc::tmem_relinquish();
-    tc::fence_before_sync();
-  }
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = *tmem_holder;
-
-  // (tensor memory is held before dependents may start: a dependent kernel
-  // that took it first would wait for this one, and this one for it)
-  pdl_launch_dependents();
-  pdl_wait();
+  const uint32_t tmem = su_begin<D>(bars, 1, warp);
 
   // item: row tiles from the last (longest) to the first, then pairs, splits
   const int sp = blockIdx.x % p.splits;
-  int rest = blockIdx.x / p.splits;
+  const int rest = blockIdx.x / p.splits;
   const int pair = rest % (p.B * p.G);
   const int tile = p.row_tiles - 1 - rest / (p.B * p.G);
   const int b = pair / p.G, g = pair - b * p.G;
@@ -135,73 +238,52 @@ attn_stats_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   float* lse_g = p.lse + (long long)(b * p.H + g * p.rep) * p.runs * SU_RUN;
   auto run_of = [&](int r) { return r / p.rep; };
   auto head_of = [&](int r) { return r % p.rep; };
-  const bool active = r0 < n_runs;
-  const bool two = r1 < n_runs;
+  const bool active = r0 < n_runs, two = r1 < n_runs;
   const int last_q = min(R.n - 1, R.lo + (run_of(two ? r1 : r0) + 1) * SU_RUN - 1);
-  const int nt = last_q / SU_KEYS + 1;
+  const int nt = last_q / SU_RUN + 1;      // 64-key tiles that some row sees
   const int t0 = (int)((long long)sp * nt / p.splits);
-  const int t1 = active ? (int)((long long)(sp + 1) * nt / p.splits) : t0;
-
+  const int n = active ? (int)((long long)(sp + 1) * nt / p.splits) - t0 : 0;
 
   if (warp == 0) {
-    if (lane == 0 && t1 > t0) {
-      tc::mbar_expect_tx(q_full, (two ? 2 : 1) * L::KB * L::RUN_B);
+    if (lane == 0 && n > 0) {
+      tc::mbar_expect_tx(&bars->a_full, (two ? 2 : 1) * L::KB * L::RUN_B);
       for (int i = 0; i < (two ? 2 : 1); ++i) {
         const int r = r0 + i;
         for (int kb = 0; kb < L::KB; ++kb)
-          tc::tma_load_2d(smem + kb * L::KEY_B + i * L::RUN_B, &tmQ, q_full, (g * p.rep + head_of(r)) * D + 64 * kb,
-                          b * p.S + R.lo + run_of(r) * SU_RUN);
+          tc::tma_load_2d(smem + kb * L::ROWS_B + i * L::RUN_B, &tmQ, &bars->a_full,
+                          (g * p.rep + head_of(r)) * D + 64 * kb, b * p.S + R.lo + run_of(r) * SU_RUN);
       }
-      for (int j = t0; j < t1; ++j) {
-        const int k = j - t0, st = k % L::KST;
-        if (!tc::mbar_wait(k_empty + st, ((uint32_t)(k / L::KST) & 1u) ^ 1u, abort_flag, p.status)) break;
-        tc::mbar_expect_tx(k_full + st, L::KB * L::KEY_B);
+      for (int k = 0; k < n; ++k) {
+        const int st = k % L::NST;
+        if (!tc::mbar_wait(bars->empty + st, ((uint32_t)(k / L::NST) & 1u) ^ 1u, &bars->abort_flag, p.status)) break;
+        tc::mbar_expect_tx(bars->full + st, L::KB * L::RUN_B);
         for (int kb = 0; kb < L::KB; ++kb)
-          tc::tma_load_2d(smem + L::ST_K + (st * L::KB + kb) * L::KEY_B, &tmK, k_full + st, g * D + 64 * kb,
-                          b * p.S_max + j * SU_KEYS);
+          tc::tma_load_2d(smem + L::RING + (st * L::KB + kb) * L::RUN_B, &tmK, bars->full + st, g * D + 64 * kb,
+                          b * p.S_max + (t0 + k) * SU_RUN);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && t1 > t0) {
-      constexpr uint32_t IDESC = tc::idesc_bf16(SU_KEYS, false);
-      const uint32_t sq = tc::smem_u32(smem);
-      bool ok = tc::mbar_wait(q_full, 0, abort_flag, p.status);
-      for (int k = 0; k < t1 - t0 && ok; ++k) {
-        const int st = k % L::KST, sb = k & 1;
-        if (!(ok = tc::mbar_wait(k_full + st, (uint32_t)(k / L::KST) & 1u, abort_flag, p.status))) break;
-        if (!(ok = tc::mbar_wait(s_empty + sb, ((uint32_t)(k >> 1) & 1u) ^ 1u, abort_flag, p.status))) break;
-        tc::fence_after_sync();
-        const uint32_t sk = tc::smem_u32(smem + L::ST_K + st * L::KB * L::KEY_B);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t ad = tc::sdesc_sw128(sq + (kk >> 2) * L::KEY_B + (kk & 3) * 32, 16, 1024);
-          const uint64_t bd = tc::sdesc_sw128(sk + (kk >> 2) * L::KEY_B + (kk & 3) * 32, 16, 1024);
-          tc::mma_bf16(tmem + sb * SU_KEYS, ad, bd, IDESC, kk > 0 ? 1u : 0u);
-        }
-        tc::mma_commit(s_full + sb);
-        tc::mma_commit(k_empty + st);
-      }
-      tc::mma_commit(drain);
-      const long long c0 = clock64();
-      while (!tc::mbar_try_wait(drain, 0) && clock64() - c0 < tc::kWaitCycles) {}
-    }
+    if (lane == 0 && n > 0) su_products<D>(bars, smem, tmem, n, p.status);
   } else if (active) {
-    const int quad = warp & 3, hf = (warp - 2) >> 2;
+    // two groups of four warps take the tiles in turn, a thread a row
+    const int quad = warp & 3, grp = (warp - 2) >> 2;
     const int row = quad * 32 + lane;
     const int r = r0 + (row >> 6);
     const int q = R.lo + run_of(r) * SU_RUN + (row & 63);  // query position
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     const float sc = p.scale_log2;
     float m = -INFINITY, l = 0.f;
-    bool ok = true;
-    for (int k = 0; k < t1 - t0; ++k) {
-      const int sb = k & 1, key0 = (t0 + k) * SU_KEYS + hf * 64;
-      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(s_full + sb, (uint32_t)(k >> 1) & 1u, abort_flag, p.status));
+    bool ok = n > 0;
+    if (grp == 0 && n > 0) ok = su_a_to_tmem<D>(bars, smem, tmem, row, lane, p.status);
+    for (int k = grp; k < n; k += 2) {
+      const int sb = k % L::NS, key0 = (t0 + k) * SU_RUN;
+      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->s_full + sb, (uint32_t)(k / L::NS) & 1u, &bars->abort_flag,
+                                                       p.status));
       float s[64];
       if (ok) {
         tc::fence_after_sync();
-        tc::tmem_ld32(tmem + lane_base + sb * SU_KEYS + hf * 64, reinterpret_cast<uint32_t*>(s));
-        tc::tmem_ld32(tmem + lane_base + sb * SU_KEYS + hf * 64 + 32, reinterpret_cast<uint32_t*>(s + 32));
+        tc::tmem_ld32(tmem + lane_base + L::TM_S + sb * SU_RUN, reinterpret_cast<uint32_t*>(s));
+        tc::tmem_ld32(tmem + lane_base + L::TM_S + sb * SU_RUN + 32, reinterpret_cast<uint32_t*>(s + 32));
         tc::tmem_ld_wait();
         tc::reg_fence<64>(s);
       } else {
@@ -210,16 +292,24 @@ attn_stats_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(s_empty + sb);
-      if (key0 + 63 > q) {
+      if (lane == 0) tc::mbar_arrive(bars->s_empty + sb);
+      // (a branch of its own for tiles on the diagonal: as selects in the one
+      // path, the mask cost every tile four instructions a score)
+      float mx;
+      if (__any_sync(0xffffffffu, key0 + 63 > q)) {
+        mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (key0 + c > q) s[c] = -INFINITY;
+        for (int c = 0; c < 64; ++c) {
+          s[c] = key0 + c > q ? -INFINITY : s[c];
+          mx = fmaxf(mx, s[c]);
+        }
+      } else {
+        float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < 64; c += 2) m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], s[c], s[c + 1]);
+        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       }
-      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 64; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sc;
+      mx *= sc;
       if (mx > m) {
         l *= ex2f(m - mx);
         m = mx;
@@ -227,20 +317,23 @@ attn_stats_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const float e = m == -INFINITY ? 0.f : -m;
       float a4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 64; ++c) a4[c & 3] += ex2f(fmaf(s[c], sc, e));
+      for (int c = 0; c < 64; c += 2) {
+        fma2(s[c], s[c + 1], sc, e, e);
+        add2(a4[c & 2], a4[(c & 2) + 1], ex2f(s[c]), ex2f(s[c + 1]));
+      }
       l += (a4[0] + a4[1]) + (a4[2] + a4[3]);
     }
-    xch[hf * 128 + row] = make_float2(m, l);
+    if (grp == 1) xch[row] = make_float2(m, l);
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (hf == 0) {
-      const float2 o = xch[128 + row];
+    if (grp == 0) {
+      const float2 o = xch[row];
       const float M = fmaxf(m, o.x);
       const float e = M == -INFINITY ? 0.f : M;
       const float sum = l * ex2f(m - e) + o.y * ex2f(o.x - e);
       if (p.splits == 1) {
         if (r < n_runs)
           lse_g[(long long)head_of(r) * p.runs * SU_RUN + run_of(r) * SU_RUN + (row & 63)] =
-              q < R.n ? M + log2f(sum) : INFINITY;
+              q < R.n ? -(M + log2f(sum)) : -INFINITY;
       } else {
         __stcg(p.part + (((long long)pair * p.row_tiles + tile) * p.splits + sp) * 128 + row, make_float2(M, sum));
       }
@@ -251,37 +344,29 @@ attn_stats_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       if (threadIdx.x == 64) {
         int* cnt = p.counters + (long long)pair * p.row_tiles + tile;
         const int old = atomicAdd(cnt, 1);
-        *s_last = old == p.splits - 1;
+        bars->last = old == p.splits - 1;
         if (old == p.splits - 1) *cnt = 0;
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (*s_last && hf == 0 && r < n_runs) {
+      if (bars->last && grp == 0 && r < n_runs) {
         __threadfence();
         const float2* src = p.part + ((long long)pair * p.row_tiles + tile) * p.splits * 128 + row;
         float M = -INFINITY;
+#pragma unroll 8
         for (int i = 0; i < p.splits; ++i) M = fmaxf(M, __ldcg(src + i * 128).x);
         const float e = M == -INFINITY ? 0.f : M;
         float sum = 0.f;
+#pragma unroll 8
         for (int i = 0; i < p.splits; ++i) {
           const float2 o = __ldcg(src + i * 128);
           sum += o.y * ex2f(o.x - e);
         }
         lse_g[(long long)head_of(r) * p.runs * SU_RUN + run_of(r) * SU_RUN + (row & 63)] =
-            q < R.n ? M + log2f(sum) : INFINITY;
+            q < R.n ? -(M + log2f(sum)) : -INFINITY;
       }
     }
   }
-  tc::fence_before_sync();
-  __syncthreads();
-  if (*abort_flag && warp == 0 && lane == 0) {
-    // let copies still in flight land before shared memory is released
-    const long long c0 = clock64();
-    while (clock64() - c0 < 2000000) {}
-  }
-  if (warp == 1) {
-    tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 256);
-  }
+  su_end<D>(bars, tmem, warp, lane);
 }
 
 template <int D>
@@ -291,143 +376,109 @@ attn_sums_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   using L = SuLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::SM_BAR);
-  uint64_t* q_full = k_full + 1;           // [QST]
-  uint64_t* q_empty = q_full + L::QST;     // [QST] the MMA and the 8 softmax warps
-  uint64_t* s_full = q_empty + L::QST;     // [4]
-  uint64_t* s_empty = s_full + 4;          // [4]
-  uint64_t* drain = s_empty + 4;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  float* xch = reinterpret_cast<float*>(smem + L::SM_BAR + 256);  // [128]
+  SuBars<D>* bars = reinterpret_cast<SuBars<D>*>(smem + L::BAR);
+  float* xch = reinterpret_cast<float*>(smem + L::XCH);  // [128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (threadIdx.x == 0) {
-    tc::mbar_init(k_full, 1);
-    for (int i = 0; i < L::QST; ++i) { tc::mbar_init(q_full + i, 1); tc::mbar_init(q_empty + i, 9); }
-    for (int i = 0; i < 4; ++i) { tc::mbar_init(s_full + i, 1); tc::mbar_init(s_empty + i, 8); }
-    tc::mbar_init(drain, 1);
-    *abort_flag = 0;
-    tc::fence_barrier_init();
-  }
-  if (warp == 1) {
-    tc::tmem_alloc(tmem_holder, 256);
-    tc::tmem_relinquish();
-    tc::fence_before_sync();
-  }
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = *tmem_holder;
-
-  pdl_launch_dependents();  // tensor memory is held (see attn_stats_kernel)
-  pdl_wait();
+  const uint32_t tmem = su_begin<D>(bars, 5, warp);      // the MMA and the four warps that read the lse
 
   const int pair = blockIdx.x % (p.B * p.G), kt = blockIdx.x / (p.B * p.G);
   const int b = pair / p.G, g = pair - b * p.G;
   const SuRow R(p, b);
   const int key0 = kt * SU_KEYS;
-  const int run0 = key0 > R.lo ? (key0 - R.lo) / SU_RUN : 0;  // first run that sees a key
+  const int run0 = key0 > R.lo ? (key0 - R.lo) / SU_RUN : 0;     // first run that sees a key
   const int items = key0 < R.n ? (R.runs() - run0) * p.rep : 0;  // (run, head), run-major
   const float* lse_g = p.lse + (long long)(b * p.H + g * p.rep) * p.runs * SU_RUN;
 
-
   if (warp == 0) {
     if (lane == 0 && items > 0) {
-      tc::mbar_expect_tx(k_full, L::KB * L::KEY_B);
+      tc::mbar_expect_tx(&bars->a_full, L::KB * L::ROWS_B);
       for (int kb = 0; kb < L::KB; ++kb)
-        tc::tma_load_2d(smem + kb * L::KEY_B, &tmK, k_full, g * D + 64 * kb, b * p.S_max + key0);
-      for (int k = 0; k < items; ++k) {
-        const int st = k % L::QST, run = run0 + k / p.rep, h = k % p.rep;
-        if (!tc::mbar_wait(q_empty + st, ((uint32_t)(k / L::QST) & 1u) ^ 1u, abort_flag, p.status)) break;
-        tc::mbar_expect_tx(q_full + st, L::KB * L::RUN_B + SU_RUN * 4);
+        for (int i = 0; i < 2; ++i)
+          tc::tma_load_2d(smem + kb * L::ROWS_B + i * L::RUN_B, &tmK, &bars->a_full, g * D + 64 * kb,
+                          b * p.S_max + key0 + i * SU_RUN);
+      for (int k = 0, run = run0, h = 0; k < items; ++k, ++h) {
+        const int st = k % L::NST;
+        if (h == p.rep) { h = 0; ++run; }
+        if (!tc::mbar_wait(bars->empty + st, ((uint32_t)(k / L::NST) & 1u) ^ 1u, &bars->abort_flag, p.status)) break;
+        tc::mbar_expect_tx(bars->full + st, L::KB * L::RUN_B + SU_RUN * 4);
         for (int kb = 0; kb < L::KB; ++kb)
-          tc::tma_load_2d(smem + L::SM_Q + (st * L::KB + kb) * L::RUN_B, &tmQ, q_full + st,
+          tc::tma_load_2d(smem + L::RING + (st * L::KB + kb) * L::RUN_B, &tmQ, bars->full + st,
                           (g * p.rep + h) * D + 64 * kb, b * p.S + R.lo + run * SU_RUN);
         const float* src = lse_g + (long long)h * p.runs * SU_RUN + run * SU_RUN;
         asm volatile(
             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                tc::smem_u32(smem + L::SM_LSE + st * SU_RUN * 4)),
-            "l"(src), "r"(SU_RUN * 4), "r"(tc::smem_u32(q_full + st))
+                tc::smem_u32(smem + L::LSE + st * SU_RUN * 4)),
+            "l"(src), "r"(SU_RUN * 4), "r"(tc::smem_u32(bars->full + st))
             : "memory");
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && items > 0) {
-      constexpr uint32_t IDESC = tc::idesc_bf16(SU_RUN, false);
-      const uint32_t sk = tc::smem_u32(smem);
-      bool ok = tc::mbar_wait(k_full, 0, abort_flag, p.status);
-      for (int k = 0; k < items && ok; ++k) {
-        const int st = k % L::QST, sb = k & 3;
-        if (!(ok = tc::mbar_wait(q_full + st, (uint32_t)(k / L::QST) & 1u, abort_flag, p.status))) break;
-        if (!(ok = tc::mbar_wait(s_empty + sb, ((uint32_t)(k >> 2) & 1u) ^ 1u, abort_flag, p.status))) break;
-        tc::fence_after_sync();
-        const uint32_t sq = tc::smem_u32(smem + L::SM_Q + st * L::KB * L::RUN_B);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t ad = tc::sdesc_sw128(sk + (kk >> 2) * L::KEY_B + (kk & 3) * 32, 16, 1024);
-          const uint64_t bd = tc::sdesc_sw128(sq + (kk >> 2) * L::RUN_B + (kk & 3) * 32, 16, 1024);
-          tc::mma_bf16(tmem + sb * SU_RUN, ad, bd, IDESC, kk > 0 ? 1u : 0u);
-        }
-        tc::mma_commit(s_full + sb);
-        tc::mma_commit(q_empty + st);
-      }
-      tc::mma_commit(drain);
-      const long long c0 = clock64();
-      while (!tc::mbar_try_wait(drain, 0) && clock64() - c0 < tc::kWaitCycles) {}
-    }
+    if (lane == 0 && items > 0) su_products<D>(bars, smem, tmem, items, p.status);
   } else {
-    const int quad = warp & 3, hf = (warp - 2) >> 2;
+    // two groups of four warps take the runs in turn, a thread a key
+    const int quad = warp & 3, grp = (warp - 2) >> 2;
     const int row = quad * 32 + lane, key = key0 + row;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     const float sc = p.scale_log2;
     float total = 0.f;
-    bool ok = true;
-    for (int k = 0; k < items; ++k) {
-      const int st = k % L::QST, sb = k & 3;
-      const int q0 = R.lo + (run0 + k / p.rep) * SU_RUN + hf * 32;  // position of column 0
-      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(q_full + st, (uint32_t)(k / L::QST) & 1u, abort_flag, p.status));
-      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(s_full + sb, (uint32_t)(k >> 2) & 1u, abort_flag, p.status));
-      float s[32], e[32];
+    bool ok = items > 0;
+    if (grp == 0 && items > 0) ok = su_a_to_tmem<D>(bars, smem, tmem, row, lane, p.status);
+    int q0 = R.lo + run0 * SU_RUN, h = grp;  // position of the run's first query
+    for (int k = grp; k < items; k += 2, h += 2) {
+      const int st = k % L::NST, sb = k % L::NS;
+      while (h >= p.rep) { h -= p.rep; q0 += SU_RUN; }
+      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->full + st, (uint32_t)(k / L::NST) & 1u, &bars->abort_flag,
+                                                       p.status));
+      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->s_full + sb, (uint32_t)(k / L::NS) & 1u, &bars->abort_flag,
+                                                       p.status));
+      float s[64];
       if (ok) {
         tc::fence_after_sync();
-        tc::tmem_ld32(tmem + lane_base + sb * SU_RUN + hf * 32, reinterpret_cast<uint32_t*>(s));
-        const float4* ls = reinterpret_cast<const float4*>(smem + L::SM_LSE + st * SU_RUN * 4) + hf * 8;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) *reinterpret_cast<float4*>(e + 4 * c) = ls[c];
+        tc::tmem_ld32(tmem + lane_base + L::TM_S + sb * SU_RUN, reinterpret_cast<uint32_t*>(s));
+        tc::tmem_ld32(tmem + lane_base + L::TM_S + sb * SU_RUN + 32, reinterpret_cast<uint32_t*>(s + 32));
         tc::tmem_ld_wait();
-        tc::reg_fence<32>(s);
+        tc::reg_fence<64>(s);
       } else {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] = e[c] = 0.f;
+        for (int c = 0; c < 64; ++c) s[c] = 0.f;
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) { tc::mbar_arrive(s_empty + sb); tc::mbar_arrive(q_empty + st); }
-      if (q0 < key0 + SU_KEYS || q0 + 32 > R.n) {
+      if (lane == 0) tc::mbar_arrive(bars->s_empty + sb);
+      const float4* ls = reinterpret_cast<const float4*>(smem + L::LSE + st * SU_RUN * 4);
+      float a4[4] = {0.f, 0.f, 0.f, 0.f};
+      if (q0 < key0 + SU_KEYS || q0 + SU_RUN > R.n) {
         // queries before the key, and rows behind the sequence (whatever they hold)
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (q0 + c < key || q0 + c >= R.n) { s[c] = -INFINITY; e[c] = 0.f; }
-      }
-      float a4[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < 64; c += 4) {
+          const float4 e = ls[c >> 2];
+          const float x[4] = {fmaf(s[c], sc, e.x), fmaf(s[c + 1], sc, e.y), fmaf(s[c + 2], sc, e.z),
+                              fmaf(s[c + 3], sc, e.w)};
 #pragma unroll
-      for (int c = 0; c < 32; ++c) a4[c & 3] += ex2f(fmaf(s[c], sc, -e[c]));
+          for (int i = 0; i < 4; ++i) {
+            const float y = ex2f(x[i]);
+            a4[i] += q0 + c + i < key || q0 + c + i >= R.n ? 0.f : y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 e = ls[c >> 2];
+          fma2(s[c], s[c + 1], sc, e.x, e.y);
+          fma2(s[c + 2], s[c + 3], sc, e.z, e.w);
+          add2(a4[0], a4[1], ex2f(s[c]), ex2f(s[c + 1]));
+          add2(a4[2], a4[3], ex2f(s[c + 2]), ex2f(s[c + 3]));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bars->empty + st);
       total += (a4[0] + a4[1]) + (a4[2] + a4[3]);
     }
-    if (hf == 1) xch[row] = total;
+    if (grp == 1) xch[row] = total;
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (hf == 0 && ok && key < R.n) p.weights[(long long)pair * p.w_stride + key] = total + xch[row];
+    if (grp == 0 && ok && key < R.n) p.weights[(long long)pair * p.w_stride + key] = total + xch[row];
   }
-  tc::fence_before_sync();
-  __syncthreads();
-  if (*abort_flag && warp == 0 && lane == 0) {
-    const long long c0 = clock64();
-    while (clock64() - c0 < 2000000) {}
-  }
-  if (warp == 1) {
-    tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 256);
-  }
+  su_end<D>(bars, tmem, warp, lane);
 }
 
 template <int D>
@@ -458,22 +509,21 @@ int launch_sums(const AttnSumsParams& a, int sm_count, cudaStream_t stream) {
   p.lse = a.ws;
   p.part = reinterpret_cast<float2*>(a.ws + lse);
   p.counters = a.counters;
-  CUtensorMap mq, mk_s, mk;
+  CUtensorMap mq, mk;
   const long long HD = (long long)a.H * D, GD = (long long)a.G * D;
   FSVD_TRY(encode_map(&mq, a.q, (long long)a.B * a.S, HD, HD, 64, SU_RUN, true));
-  FSVD_TRY(encode_map(&mk, a.k, (long long)a.B * a.S_max, GD, GD, 64, SU_KEYS, true));
-  mk_s = mk;
+  FSVD_TRY(encode_map(&mk, a.k, (long long)a.B * a.S_max, GD, GD, 64, SU_RUN, true));
   auto k1 = attn_stats_kernel<D>;
   auto k2 = attn_sums_kernel<D>;
   static SmemAttrOnce once1, once2;
-  FSVD_TRY(set_smem_once(once1, k1, L::ST_SMEM));
-  FSVD_TRY(set_smem_once(once2, k2, L::SM_SMEM));
+  FSVD_TRY(set_smem_once(once1, k1, L::SMEM));
+  FSVD_TRY(set_smem_once(once2, k2, L::SMEM));
   const double pq = (double)p.window * a.S - 0.5 * (double)p.window * p.window;  // visible pairs
   const double bytes = 2.0 * D * a.B * ((double)p.window * a.H + (double)a.S * a.G);
   const LaunchTag t1{"attn_stats", bytes + 4.0 * lse, 2.0 * D * heads * pq};
   const LaunchTag t2{"attn_sums", bytes + 4.0 * lse + 4.0 * pairs * a.S, 2.0 * D * heads * pq};
-  FSVD_TRY(launch_pdl(t1, k1, dim3((unsigned)(tiles * splits)), dim3(SU_THREADS), (size_t)L::ST_SMEM, stream, mq, mk_s, p));
-  return launch_pdl(t2, k2, dim3((unsigned)(pairs * key_tiles)), dim3(SU_THREADS), (size_t)L::SM_SMEM, stream, mq, mk, p);
+  FSVD_TRY(launch_pdl(t1, k1, dim3((unsigned)(tiles * splits)), dim3(SU_THREADS), (size_t)L::SMEM, stream, mq, mk, p));
+  return launch_pdl(t2, k2, dim3((unsigned)(pairs * key_tiles)), dim3(SU_THREADS), (size_t)L::SMEM, stream, mq, mk, p);
 }
 
 }  // namespace
