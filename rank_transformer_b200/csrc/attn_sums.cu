@@ -94,7 +94,7 @@ struct SuLayout {
   static constexpr int LSE = RING + NST * KB * RUN_B;      // the runs' -lse (sums)
   static constexpr int BAR = LSE + NST * SU_RUN * 4;
   static constexpr int XCH = BAR + 256;                    // exchange between the two threads of a row
-  static constexpr int SMEM = 1024 + XCH + 128 * 8;
+  static constexpr int SMEM = 1024 + XCH + 2 * 128 * 8;
   static constexpr uint32_t TM_S = 64;          // tensor memory: A in [0, D / 2), S buffers of 64 from here
   static constexpr int NS = 3;
 };
@@ -102,7 +102,7 @@ struct SuLayout {
 // Barriers of a CTA, in shared memory.
 template <int D>
 struct SuBars {
-  uint64_t a_full, a_tmem, full[SuLayout<D>::NST], empty[SuLayout<D>::NST];
+  uint64_t a_full, a_empty, a_tmem, a_free, full[SuLayout<D>::NST], empty[SuLayout<D>::NST];
   uint64_t s_full[SuLayout<D>::NS], s_empty[SuLayout<D>::NS], drain;
   uint32_t tmem;
   int abort_flag, last;
@@ -115,7 +115,9 @@ template <int D>
 __device__ __forceinline__ uint32_t su_begin(SuBars<D>* bars, int readers, int warp) {
   if (threadIdx.x == 0) {
     tc::mbar_init(&bars->a_full, 1);
+    tc::mbar_init(&bars->a_empty, 4);
     tc::mbar_init(&bars->a_tmem, 4);
+    tc::mbar_init(&bars->a_free, 1);
     for (int i = 0; i < SuLayout<D>::NST; ++i) { tc::mbar_init(bars->full + i, 1); tc::mbar_init(bars->empty + i, readers); }
     for (int i = 0; i < SuLayout<D>::NS; ++i) { tc::mbar_init(bars->s_full + i, 1); tc::mbar_init(bars->s_empty + i, 4); }
     tc::mbar_init(&bars->drain, 1);
@@ -148,19 +150,20 @@ __device__ __forceinline__ void su_end(SuBars<D>* bars, uint32_t tmem, int warp,
   }
 }
 
-// The MMA warp's lane: `n` products A . run^T (runs through the ring) into the
-// S buffers in turn.
+// The MMA warp's lane.  Item j (of those with work): `n` products A . run^T
+// (runs through the ring) into the S buffers in turn; t counts the CTA's
+// products so far.
 template <int D>
-__device__ __forceinline__ void su_products(SuBars<D>* bars, uint8_t* smem, uint32_t tmem, int n, int* status) {
+__device__ __forceinline__ bool su_products(SuBars<D>* bars, uint8_t* smem, uint32_t tmem, int j, int t, int n,
+                                            int* status) {
   using L = SuLayout<D>;
   constexpr uint32_t IDESC = tc::idesc_bf16(SU_RUN, false);
   volatile int* abort_flag = &bars->abort_flag;
-  bool ok = tc::mbar_wait(&bars->a_tmem, 0, abort_flag, status);
-  int st = 0, sb = 0;
-  uint32_t ph = 0, sph = 0;
-  for (int k = 0; k < n && ok; ++k) {
-    if (!(ok = tc::mbar_wait(bars->full + st, ph, abort_flag, status))) break;
-    if (!(ok = tc::mbar_wait(bars->s_empty + sb, sph ^ 1u, abort_flag, status))) break;
+  if (!tc::mbar_wait(&bars->a_tmem, (uint32_t)j & 1u, abort_flag, status)) return false;
+  for (int k = t; k < t + n; ++k) {
+    const int st = k % L::NST, sb = k % L::NS;
+    if (!tc::mbar_wait(bars->full + st, (uint32_t)(k / L::NST) & 1u, abort_flag, status)) return false;
+    if (!tc::mbar_wait(bars->s_empty + sb, ((uint32_t)(k / L::NS) & 1u) ^ 1u, abort_flag, status)) return false;
     tc::fence_after_sync();
     const uint32_t sq = tc::smem_u32(smem + L::RING + st * L::KB * L::RUN_B);
 #pragma unroll
@@ -169,22 +172,29 @@ __device__ __forceinline__ void su_products(SuBars<D>* bars, uint8_t* smem, uint
                       tc::sdesc_sw128(sq + (kk >> 2) * L::RUN_B + (kk & 3) * 32, 16, 1024), IDESC, kk > 0 ? 1u : 0u);
     tc::mma_commit(bars->s_full + sb);
     tc::mma_commit(bars->empty + st);
-    if (++st == L::NST) { st = 0; ph ^= 1u; }
-    if (++sb == L::NS) { sb = 0; sph ^= 1u; }
   }
+  tc::mma_commit(&bars->a_free);  // the item's products are done: A may be overwritten
+  return true;
+}
+template <int D>
+__device__ __forceinline__ void su_drain(SuBars<D>* bars) {
   tc::mma_commit(&bars->drain);
   const long long c0 = clock64();
   while (!tc::mbar_try_wait(&bars->drain, 0) && clock64() - c0 < tc::kWaitCycles) {}
 }
 
-// Four warps: the A tile from shared memory (128-byte swizzle) into tensor
-// memory, row r in lane r, two bf16 per column.
+// Four warps: item j's A tile from shared memory (128-byte swizzle) into
+// tensor memory, row r in lane r, two bf16 per column.
 template <int D>
-__device__ __forceinline__ bool su_a_to_tmem(SuBars<D>* bars, const uint8_t* smem, uint32_t tmem, int row, int lane,
+__device__ __forceinline__ bool su_a_to_tmem(SuBars<D>* bars, const uint8_t* smem, uint32_t tmem, int j, int row, int lane,
                                              int* status) {
   using L = SuLayout<D>;
-  const bool ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->a_full, 0, &bars->abort_flag, status));
+  volatile int* abort_flag = &bars->abort_flag;
+  bool ok = tc::mbar_wait(&bars->a_full, (uint32_t)j & 1u, abort_flag, status);
+  if (j > 0) ok = tc::mbar_wait(&bars->a_free, (uint32_t)(j - 1) & 1u, abort_flag, status) && ok;
+  ok = __all_sync(0xffffffffu, ok);
   if (ok) {
+    tc::fence_after_sync();
 #pragma unroll
     for (int kb = 0; kb < L::KB; ++kb) {
       uint32_t r[32];
@@ -199,19 +209,72 @@ __device__ __forceinline__ bool su_a_to_tmem(SuBars<D>* bars, const uint8_t* sme
   }
   tc::fence_before_sync();
   __syncwarp();
-  if (lane == 0) tc::mbar_arrive(&bars->a_tmem);
+  if (lane == 0) { tc::mbar_arrive(&bars->a_tmem); tc::mbar_arrive(&bars->a_empty); }
   return ok;
 }
 
-// Sequence geometry of one batch row.
-struct SuRow {
-  int n, lo;  // tokens, first query of the window
-  __device__ SuRow(const SuParams& p, int b) {
-    n = p.lens ? p.lens[b] : p.S;
-    n = n < 0 ? 0 : (n > p.S ? p.S : n);
-    lo = n > p.window ? n - p.window : 0;
+// Persistent CTAs walk the items i G + c (odd rounds: i G + G - 1 - c) of a
+// list that begins with the longest ones, so that long and short ones pair up.
+// Every role walks the list by itself; an item with nothing to do is passed
+// over by all of them.
+struct SuItem {
+  int pair, b, g, t;  // (batch row, KV head); row tile (stats) or key tile (sums)
+  int sp;             // key split (stats)
+  int len;            // tokens of the batch row, as read
+};
+__device__ __forceinline__ int su_index(int i) {
+  const int G = gridDim.x, c = blockIdx.x;
+  return i * G + ((i & 1) ? G - 1 - c : c);
+}
+__device__ __forceinline__ SuItem su_item(const SuParams& p, int k, bool stats) {
+  SuItem it;
+  const int pairs = p.B * p.G;
+  int rest = k;
+  it.sp = 0;
+  if (stats) {
+    rest = k / p.splits;
+    it.sp = k - rest * p.splits;
   }
-  __device__ int runs() const { return (n - lo + SU_RUN - 1) / SU_RUN; }
+  it.t = rest / pairs;
+  it.pair = rest - it.t * pairs;
+  if (stats) it.t = p.row_tiles - 1 - it.t;  // the last rows see the most keys
+  it.b = it.pair / p.G;
+  it.g = it.pair - it.b * p.G;
+  it.len = p.lens ? p.lens[it.b] : p.S;
+  return it;
+}
+// The window of an item's sequence: tokens, first query, runs of 64 queries.
+struct SuRow {
+  int n, lo, runs;
+  __device__ SuRow(const SuParams& p, int len) {
+    n = len < 0 ? 0 : (len > p.S ? p.S : len);
+    lo = n > p.window ? n - p.window : 0;
+    runs = (n - lo + SU_RUN - 1) / SU_RUN;
+  }
+};
+// Stats: the item's two (run, head) of the run-major list, and its 64-key
+// tiles t0 .. t0 + n (those some row of it sees, one split's part).
+struct SuStats {
+  int run[2], head[2], two, t0, n;
+  __device__ SuStats(const SuParams& p, const SuItem& it, const SuRow& R) {
+    const int r0 = 2 * it.t, all = R.runs * p.rep;
+    run[0] = r0 / p.rep; head[0] = r0 - run[0] * p.rep;
+    run[1] = (r0 + 1) / p.rep; head[1] = r0 + 1 - run[1] * p.rep;
+    two = r0 + 1 < all;
+    const int last_q = min(R.n - 1, R.lo + ((two ? run[1] : run[0]) + 1) * SU_RUN - 1), nt = last_q / SU_RUN + 1;
+    t0 = (int)((long long)it.sp * nt / p.splits);
+    n = r0 < all ? (int)((long long)(it.sp + 1) * nt / p.splits) - t0 : 0;
+  }
+  __device__ bool live(const SuParams& p, const SuItem& it, const SuRow& R) const { return 2 * it.t < R.runs * p.rep; }
+};
+// Sums: first run that sees a key of the tile, and the (run, head) from it on.
+struct SuSums {
+  int key0, run0, n;
+  __device__ SuSums(const SuParams& p, const SuItem& it, const SuRow& R) {
+    key0 = it.t * SU_KEYS;
+    run0 = key0 > R.lo ? (key0 - R.lo) / SU_RUN : 0;
+    n = key0 < R.n ? (R.runs - run0) * p.rep : 0;
+  }
 };
 
 template <int D>
@@ -222,61 +285,75 @@ attn_stats_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   SuBars<D>* bars = reinterpret_cast<SuBars<D>*>(smem + L::BAR);
-  float2* xch = reinterpret_cast<float2*>(smem + L::XCH);  // [128]
+  float2* xch = reinterpret_cast<float2*>(smem + L::XCH);  // [2][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t tmem = su_begin<D>(bars, 1, warp);
-
-  // item: row tiles from the last (longest) to the first, then pairs, splits
-  const int sp = blockIdx.x % p.splits;
-  const int rest = blockIdx.x / p.splits;
-  const int pair = rest % (p.B * p.G);
-  const int tile = p.row_tiles - 1 - rest / (p.B * p.G);
-  const int b = pair / p.G, g = pair - b * p.G;
-  const SuRow R(p, b);
-  const int n_runs = R.runs() * p.rep;     // (run, head) in run-major order
-  const int r0 = 2 * tile, r1 = 2 * tile + 1;
-  float* lse_g = p.lse + (long long)(b * p.H + g * p.rep) * p.runs * SU_RUN;
-  auto run_of = [&](int r) { return r / p.rep; };
-  auto head_of = [&](int r) { return r % p.rep; };
-  const bool active = r0 < n_runs, two = r1 < n_runs;
-  const int last_q = min(R.n - 1, R.lo + (run_of(two ? r1 : r0) + 1) * SU_RUN - 1);
-  const int nt = last_q / SU_RUN + 1;      // 64-key tiles that some row sees
-  const int t0 = (int)((long long)sp * nt / p.splits);
-  const int n = active ? (int)((long long)(sp + 1) * nt / p.splits) - t0 : 0;
+  const int items = p.B * p.G * p.row_tiles * p.splits;
 
   if (warp == 0) {
-    if (lane == 0 && n > 0) {
-      tc::mbar_expect_tx(&bars->a_full, (two ? 2 : 1) * L::KB * L::RUN_B);
-      for (int i = 0; i < (two ? 2 : 1); ++i) {
-        const int r = r0 + i;
-        for (int kb = 0; kb < L::KB; ++kb)
-          tc::tma_load_2d(smem + kb * L::ROWS_B + i * L::RUN_B, &tmQ, &bars->a_full,
-                          (g * p.rep + head_of(r)) * D + 64 * kb, b * p.S + R.lo + run_of(r) * SU_RUN);
-      }
-      for (int k = 0; k < n; ++k) {
-        const int st = k % L::NST;
-        if (!tc::mbar_wait(bars->empty + st, ((uint32_t)(k / L::NST) & 1u) ^ 1u, &bars->abort_flag, p.status)) break;
-        tc::mbar_expect_tx(bars->full + st, L::KB * L::RUN_B);
-        for (int kb = 0; kb < L::KB; ++kb)
-          tc::tma_load_2d(smem + L::RING + (st * L::KB + kb) * L::RUN_B, &tmK, bars->full + st, g * D + 64 * kb,
-                          b * p.S_max + (t0 + k) * SU_RUN);
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = 0, j = 0, t = 0; ok && su_index(i) < items; ++i) {
+        const SuItem it = su_item(p, su_index(i), true);
+        const SuRow R(p, it.len);
+        const SuStats w(p, it, R);
+        if (w.n == 0) continue;
+        if (!(ok = tc::mbar_wait(&bars->a_empty, ((uint32_t)j & 1u) ^ 1u, &bars->abort_flag, p.status))) break;
+        tc::mbar_expect_tx(&bars->a_full, (1 + w.two) * L::KB * L::RUN_B);
+        for (int x = 0; x < 1 + w.two; ++x)
+          for (int kb = 0; kb < L::KB; ++kb)
+            tc::tma_load_2d(smem + kb * L::ROWS_B + x * L::RUN_B, &tmQ, &bars->a_full,
+                            (it.g * p.rep + w.head[x]) * D + 64 * kb, it.b * p.S + R.lo + w.run[x] * SU_RUN);
+        for (int k = t; k < t + w.n; ++k) {
+          const int st = k % L::NST;
+          if (!(ok = tc::mbar_wait(bars->empty + st, ((uint32_t)(k / L::NST) & 1u) ^ 1u, &bars->abort_flag, p.status))) break;
+          tc::mbar_expect_tx(bars->full + st, L::KB * L::RUN_B);
+          for (int kb = 0; kb < L::KB; ++kb)
+            tc::tma_load_2d(smem + L::RING + (st * L::KB + kb) * L::RUN_B, &tmK, bars->full + st, it.g * D + 64 * kb,
+                            it.b * p.S_max + (w.t0 + k - t) * SU_RUN);
+        }
+        t += w.n;
+        ++j;
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) su_products<D>(bars, smem, tmem, n, p.status);
-  } else if (active) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = 0, j = 0, t = 0; ok && su_index(i) < items; ++i) {
+        const SuItem it = su_item(p, su_index(i), true);
+        const SuRow R(p, it.len);
+        const SuStats w(p, it, R);
+        if (w.n == 0) continue;
+        ok = su_products<D>(bars, smem, tmem, j, t, w.n, p.status);
+        t += w.n;
+        ++j;
+      }
+      su_drain<D>(bars);
+    }
+  } else {
     // two groups of four warps take the tiles in turn, a thread a row
     const int quad = warp & 3, grp = (warp - 2) >> 2;
     const int row = quad * 32 + lane;
-    const int r = r0 + (row >> 6);
-    const int q = R.lo + run_of(r) * SU_RUN + (row & 63);  // query position
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     const float sc = p.scale_log2;
+    bool ok = true;
+    int i = 0, j = 0, t = 0, done = 0;  // items: of the list, with products, finished
+    SuItem next = su_item(p, min(su_index(0), items - 1), true);
+    for (; su_index(i) < items; ++i) {
+    const SuItem it = next;
+    if (su_index(i + 1) < items) next = su_item(p, su_index(i + 1), true);  // (its length arrives meanwhile)
+    const SuRow R(p, it.len);
+    const SuStats w(p, it, R);
+    if (!w.live(p, it, R)) continue;
+    const int half = row >> 6;
+    const int run = half ? w.run[1] : w.run[0], head = half ? w.head[1] : w.head[0];
+    const bool mine = half == 0 || w.two;
+    const int q = R.lo + run * SU_RUN + (row & 63);  // query position
+    float* lse = p.lse + ((long long)(it.b * p.H + it.g * p.rep + head) * p.runs + run) * SU_RUN + (row & 63);
     float m = -INFINITY, l = 0.f;
-    bool ok = n > 0;
-    if (grp == 0 && n > 0) ok = su_a_to_tmem<D>(bars, smem, tmem, row, lane, p.status);
-    for (int k = grp; k < n; k += 2) {
-      const int sb = k % L::NS, key0 = (t0 + k) * SU_RUN;
+    if (grp == 0 && w.n > 0) ok = su_a_to_tmem<D>(bars, smem, tmem, j, row, lane, p.status) && ok;
+    for (int k = t + grp; k < t + w.n; k += 2) {
+      const int sb = k % L::NS, key0 = (w.t0 + k - t) * SU_RUN;
       ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->s_full + sb, (uint32_t)(k / L::NS) & 1u, &bars->abort_flag,
                                                        p.status));
       float s[64];
@@ -323,48 +400,49 @@ attn_stats_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       }
       l += (a4[0] + a4[1]) + (a4[2] + a4[3]);
     }
-    if (grp == 1) xch[row] = make_float2(m, l);
+    t += w.n;
+    float2* x = xch + (done++ & 1) * 128 + row;  // (in turn: the last item's may still be read)
+    if (grp == 1) *x = make_float2(m, l);
     asm volatile("bar.sync 1, 256;" ::: "memory");
+    const int cell = it.pair * p.row_tiles + it.t;  // row tile of the pair
     if (grp == 0) {
-      const float2 o = xch[row];
+      const float2 o = *x;
       const float M = fmaxf(m, o.x);
       const float e = M == -INFINITY ? 0.f : M;
       const float sum = l * ex2f(m - e) + o.y * ex2f(o.x - e);
       if (p.splits == 1) {
-        if (r < n_runs)
-          lse_g[(long long)head_of(r) * p.runs * SU_RUN + run_of(r) * SU_RUN + (row & 63)] =
-              q < R.n ? -(M + log2f(sum)) : -INFINITY;
+        if (mine) *lse = q < R.n ? -(M + log2f(sum)) : -INFINITY;
       } else {
-        __stcg(p.part + (((long long)pair * p.row_tiles + tile) * p.splits + sp) * 128 + row, make_float2(M, sum));
+        __stcg(p.part + ((long long)cell * p.splits + it.sp) * 128 + row, make_float2(M, sum));
       }
     }
     if (p.splits > 1) {
       __threadfence();
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (threadIdx.x == 64) {
-        int* cnt = p.counters + (long long)pair * p.row_tiles + tile;
-        const int old = atomicAdd(cnt, 1);
+        const int old = atomicAdd(p.counters + cell, 1);
         bars->last = old == p.splits - 1;
-        if (old == p.splits - 1) *cnt = 0;
+        if (old == p.splits - 1) p.counters[cell] = 0;
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (bars->last && grp == 0 && r < n_runs) {
+      if (bars->last && grp == 0 && mine) {
         __threadfence();
-        const float2* src = p.part + ((long long)pair * p.row_tiles + tile) * p.splits * 128 + row;
+        const float2* src = p.part + (long long)cell * p.splits * 128 + row;
         float M = -INFINITY;
 #pragma unroll 8
-        for (int i = 0; i < p.splits; ++i) M = fmaxf(M, __ldcg(src + i * 128).x);
+        for (int z = 0; z < p.splits; ++z) M = fmaxf(M, __ldcg(src + z * 128).x);
         const float e = M == -INFINITY ? 0.f : M;
         float sum = 0.f;
 #pragma unroll 8
-        for (int i = 0; i < p.splits; ++i) {
-          const float2 o = __ldcg(src + i * 128);
+        for (int z = 0; z < p.splits; ++z) {
+          const float2 o = __ldcg(src + z * 128);
           sum += o.y * ex2f(o.x - e);
         }
-        lse_g[(long long)head_of(r) * p.runs * SU_RUN + run_of(r) * SU_RUN + (row & 63)] =
-            q < R.n ? -(M + log2f(sum)) : -INFINITY;
+        *lse = q < R.n ? -(M + log2f(sum)) : -INFINITY;
       }
     }
+    if (w.n > 0) ++j;
+    }  // items
   }
   su_end<D>(bars, tmem, warp, lane);
 }
@@ -377,54 +455,80 @@ attn_sums_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   SuBars<D>* bars = reinterpret_cast<SuBars<D>*>(smem + L::BAR);
-  float* xch = reinterpret_cast<float*>(smem + L::XCH);  // [128]
+  float* xch = reinterpret_cast<float*>(smem + L::XCH);  // [2][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t tmem = su_begin<D>(bars, 5, warp);      // the MMA and the four warps that read the lse
 
-  const int pair = blockIdx.x % (p.B * p.G), kt = blockIdx.x / (p.B * p.G);
-  const int b = pair / p.G, g = pair - b * p.G;
-  const SuRow R(p, b);
-  const int key0 = kt * SU_KEYS;
-  const int run0 = key0 > R.lo ? (key0 - R.lo) / SU_RUN : 0;     // first run that sees a key
-  const int items = key0 < R.n ? (R.runs() - run0) * p.rep : 0;  // (run, head), run-major
-  const float* lse_g = p.lse + (long long)(b * p.H + g * p.rep) * p.runs * SU_RUN;
+  const int items = p.B * p.G * ((p.S + SU_KEYS - 1) / SU_KEYS);
 
   if (warp == 0) {
-    if (lane == 0 && items > 0) {
-      tc::mbar_expect_tx(&bars->a_full, L::KB * L::ROWS_B);
-      for (int kb = 0; kb < L::KB; ++kb)
-        for (int i = 0; i < 2; ++i)
-          tc::tma_load_2d(smem + kb * L::ROWS_B + i * L::RUN_B, &tmK, &bars->a_full, g * D + 64 * kb,
-                          b * p.S_max + key0 + i * SU_RUN);
-      for (int k = 0, run = run0, h = 0; k < items; ++k, ++h) {
-        const int st = k % L::NST;
-        if (h == p.rep) { h = 0; ++run; }
-        if (!tc::mbar_wait(bars->empty + st, ((uint32_t)(k / L::NST) & 1u) ^ 1u, &bars->abort_flag, p.status)) break;
-        tc::mbar_expect_tx(bars->full + st, L::KB * L::RUN_B + SU_RUN * 4);
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = 0, j = 0, t = 0; ok && su_index(i) < items; ++i) {
+        const SuItem it = su_item(p, su_index(i), false);
+        const SuRow R(p, it.len);
+        const SuSums w(p, it, R);
+        if (w.n == 0) continue;
+        if (!(ok = tc::mbar_wait(&bars->a_empty, ((uint32_t)j & 1u) ^ 1u, &bars->abort_flag, p.status))) break;
+        tc::mbar_expect_tx(&bars->a_full, L::KB * L::ROWS_B);
         for (int kb = 0; kb < L::KB; ++kb)
-          tc::tma_load_2d(smem + L::RING + (st * L::KB + kb) * L::RUN_B, &tmQ, bars->full + st,
-                          (g * p.rep + h) * D + 64 * kb, b * p.S + R.lo + run * SU_RUN);
-        const float* src = lse_g + (long long)h * p.runs * SU_RUN + run * SU_RUN;
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                tc::smem_u32(smem + L::LSE + st * SU_RUN * 4)),
-            "l"(src), "r"(SU_RUN * 4), "r"(tc::smem_u32(bars->full + st))
-            : "memory");
+          for (int x = 0; x < 2; ++x)
+            tc::tma_load_2d(smem + kb * L::ROWS_B + x * L::RUN_B, &tmK, &bars->a_full, it.g * D + 64 * kb,
+                            it.b * p.S_max + w.key0 + x * SU_RUN);
+        for (int k = t, run = w.run0, h = 0; k < t + w.n; ++k, ++h) {
+          const int st = k % L::NST;
+          if (h == p.rep) { h = 0; ++run; }
+          if (!(ok = tc::mbar_wait(bars->empty + st, ((uint32_t)(k / L::NST) & 1u) ^ 1u, &bars->abort_flag, p.status))) break;
+          tc::mbar_expect_tx(bars->full + st, L::KB * L::RUN_B + SU_RUN * 4);
+          const int head = it.g * p.rep + h;
+          for (int kb = 0; kb < L::KB; ++kb)
+            tc::tma_load_2d(smem + L::RING + (st * L::KB + kb) * L::RUN_B, &tmQ, bars->full + st, head * D + 64 * kb,
+                            it.b * p.S + R.lo + run * SU_RUN);
+          const float* src = p.lse + ((long long)(it.b * p.H + head) * p.runs + run) * SU_RUN;
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                  tc::smem_u32(smem + L::LSE + st * SU_RUN * 4)),
+              "l"(src), "r"(SU_RUN * 4), "r"(tc::smem_u32(bars->full + st))
+              : "memory");
+        }
+        t += w.n;
+        ++j;
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && items > 0) su_products<D>(bars, smem, tmem, items, p.status);
+    if (lane == 0) {
+      bool ok = true;
+      for (int i = 0, j = 0, t = 0; ok && su_index(i) < items; ++i) {
+        const SuItem it = su_item(p, su_index(i), false);
+        const SuRow R(p, it.len);
+        const SuSums w(p, it, R);
+        if (w.n == 0) continue;
+        ok = su_products<D>(bars, smem, tmem, j, t, w.n, p.status);
+        t += w.n;
+        ++j;
+      }
+      su_drain<D>(bars);
+    }
   } else {
     // two groups of four warps take the runs in turn, a thread a key
     const int quad = warp & 3, grp = (warp - 2) >> 2;
-    const int row = quad * 32 + lane, key = key0 + row;
+    const int row = quad * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     const float sc = p.scale_log2;
+    bool ok = true;
+    int i = 0, j = 0, t = 0;
+    SuItem next = su_item(p, min(su_index(0), items - 1), false);
+    for (; su_index(i) < items; ++i) {
+    const SuItem it = next;
+    if (su_index(i + 1) < items) next = su_item(p, su_index(i + 1), false);  // (its length arrives meanwhile)
+    const SuRow R(p, it.len);
+    const SuSums w(p, it, R);
+    if (w.n == 0) continue;
+    const int key0 = w.key0, key = key0 + row;
     float total = 0.f;
-    bool ok = items > 0;
-    if (grp == 0 && items > 0) ok = su_a_to_tmem<D>(bars, smem, tmem, row, lane, p.status);
-    int q0 = R.lo + run0 * SU_RUN, h = grp;  // position of the run's first query
-    for (int k = grp; k < items; k += 2, h += 2) {
+    if (grp == 0) ok = su_a_to_tmem<D>(bars, smem, tmem, j, row, lane, p.status) && ok;
+    int q0 = R.lo + w.run0 * SU_RUN, h = grp;  // position of the run's first query
+    for (int k = t + grp; k < t + w.n; k += 2, h += 2) {
       const int st = k % L::NST, sb = k % L::NS;
       while (h >= p.rep) { h -= p.rep; q0 += SU_RUN; }
       ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->full + st, (uint32_t)(k / L::NST) & 1u, &bars->abort_flag,
@@ -474,9 +578,13 @@ attn_sums_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (lane == 0) tc::mbar_arrive(bars->empty + st);
       total += (a4[0] + a4[1]) + (a4[2] + a4[3]);
     }
-    if (grp == 1) xch[row] = total;
+    t += w.n;
+    ++j;
+    float* x = xch + (j & 1) * 128 + row;  // (in turn: the last item's may still be read)
+    if (grp == 1) *x = total;
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (grp == 0 && ok && key < R.n) p.weights[(long long)pair * p.w_stride + key] = total + xch[row];
+    if (grp == 0 && ok && key < R.n) p.weights[(long long)it.pair * p.w_stride + key] = total + *x;
+    }  // items
   }
   su_end<D>(bars, tmem, warp, lane);
 }
@@ -496,11 +604,10 @@ int launch_sums(const AttnSumsParams& a, int sm_count, cudaStream_t stream) {
   const long long pairs = (long long)a.B * a.G, heads = (long long)a.B * a.H;
   p.row_tiles = ceil_div(p.runs * p.rep, 2);
   const int key_tiles = ceil_div(a.S, SU_KEYS);
-  // Split the keys of a row tile until there are about two CTAs per SM slot.
-  const long long tiles = pairs * p.row_tiles;
-  long long splits = tiles > 0 ? (4LL * sm_count) / tiles : 1;
-  splits = splits < 1 ? 1 : (splits > key_tiles ? key_tiles : splits);
-  if (tiles > a.counters_cap) splits = 1;
+  // With fewer row tiles than resident CTAs (two per SM) their keys are split.
+  const long long tiles = pairs * p.row_tiles, slots = 2LL * sm_count;
+  long long splits = slots / tiles;
+  splits = splits < 1 || tiles > a.counters_cap ? 1 : (splits > 2 * key_tiles ? 2 * key_tiles : splits);
   p.splits = (int)splits;
   const long long lse = heads * p.runs * SU_RUN;
   const long long part = splits > 1 ? tiles * splits * 128 * 2 : 0;
@@ -522,8 +629,8 @@ int launch_sums(const AttnSumsParams& a, int sm_count, cudaStream_t stream) {
   const double bytes = 2.0 * D * a.B * ((double)p.window * a.H + (double)a.S * a.G);
   const LaunchTag t1{"attn_stats", bytes + 4.0 * lse, 2.0 * D * heads * pq};
   const LaunchTag t2{"attn_sums", bytes + 4.0 * lse + 4.0 * pairs * a.S, 2.0 * D * heads * pq};
-  FSVD_TRY(launch_pdl(t1, k1, dim3((unsigned)(tiles * splits)), dim3(SU_THREADS), (size_t)L::SMEM, stream, mq, mk, p));
-  return launch_pdl(t2, k2, dim3((unsigned)(pairs * key_tiles)), dim3(SU_THREADS), (size_t)L::SMEM, stream, mq, mk, p);
+  FSVD_TRY(launch_pdl(t1, k1, dim3((unsigned)(tiles * splits < slots ? tiles * splits : slots)), dim3(SU_THREADS), (size_t)L::SMEM, stream, mq, mk, p));
+  return launch_pdl(t2, k2, dim3((unsigned)(pairs * key_tiles < slots ? pairs * key_tiles : slots)), dim3(SU_THREADS), (size_t)L::SMEM, stream, mq, mk, p);
 }
 
 }  // namespace
