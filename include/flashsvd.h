@@ -609,6 +609,27 @@ FLASHSVD_API int flashsvd_layer_forward(const flashsvd_layer* L, flashsvd_bf16* 
                            const int32_t* cache_seqlens, int B, int S,
                            int S_max, int mode, flashsvd_stream stream);
 
+/* The same layer (DECODER only) over an 8-bit cache with H_kv = L->H.
+ * PREFILL_CAUSAL: as above, positions 0..S-1; the prompt's rotated keys and
+ *   its values go to the caller's k_rows, v_rows [B, S, H, D] (scratch: one
+ *   pair serves all layers) and from there into the cache.  weights (fp32
+ *   [B, H, cache S_max], or NULL) is set to what flashsvd_attn_weight_sums
+ *   gives for the last `window` >= 1 queries (entries beyond S are left
+ *   alone).  cache_seqlens and positions are not read.  S <= cache S_max.
+ * DECODE: S = 1; the token becomes token cache_seqlens[b] of the cache with
+ *   the rotary position positions[b] (device int32[B]; NULL: cache_seqlens[b];
+ *   clamped to [0, rope_rows - 1]: after an eviction a token's place in the
+ *   cache is no longer its position); k_rows, v_rows [B x H x D] receive its
+ *   rows; weights, unless NULL, are added to as in flashsvd_kv8_decode_attn.
+ *   Runs the per-stage kernels (a decode pack is not used).
+ * rope_rows: rows of L's rotary tables (PREFILL_CAUSAL: at least S). */
+FLASHSVD_API int flashsvd_layer_forward_kv8(const flashsvd_layer* L, flashsvd_bf16* x_inout,
+                                            const flashsvd_kv8* cache, flashsvd_bf16* k_rows,
+                                            flashsvd_bf16* v_rows, float* weights, int window,
+                                            const int32_t* cache_seqlens, const int32_t* positions,
+                                            int rope_rows, int B, int S, int mode,
+                                            flashsvd_stream stream);
+
 /* -------------------------------------------------------------- graphs ---
  * [v1.5] Methodology 4 (Per-Layer CUDA Graph Replay): the stable decode body
  * of one layer is captured once and replayed every step.  Buffers, B and

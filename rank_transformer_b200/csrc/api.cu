@@ -374,10 +374,51 @@ DecodeLayerDesc decode_desc(const flashsvd_layer* L) {
 }
 
 // ------------------------------------------------------- layer: decode ----
+// Stages 1-2 of a decode layer: q, k, v of rmsnorm(x) with RoPE on q and k; q
+// into the q buffer, k and v to cache row seqlens[b] of kc, vc [B, S_max, H,
+// D] or, with kv_rows, to row b of kc, vc [B x H*D] (seqlens then holds the
+// rotary positions and S_max the rows of the tables).
+int decode_qkv(const flashsvd_layer* L, const bf16* x, bf16* kc, bf16* vc, const int* seqlens, int B, int S_max,
+               int kv_rows, cudaStream_t s) {
+  const int d = L->d, r = L->q.r;
+  if (L->k.r != r || L->v.r != r) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
+  // 1) z_qkv = rmsnorm(x) . [U_q | U_k | U_v]
+  {
+    const bf16* Us[3] = {(const bf16*)L->q.U, (const bf16*)L->k.U, (const bf16*)L->v.U};
+    const int Ns[3] = {r, r, r};
+    FSVD_TRY(decode_stage1(PRO_RMSNORM, x, d, (const bf16*)L->norm1_g, L->norm_eps, Us, Ns, 3, d, B, s));
+  }
+  // 2) q, k, v = z . V (RoPE on q, k)
+  GvParams p = gv_base();
+  p.K = r; p.nprob = 3;
+  const bf16* Vs[3] = {(const bf16*)L->q.V, (const bf16*)L->k.V, (const bf16*)L->v.V};
+  for (int i = 0; i < 3; ++i) {
+    p.prob[i].W = Vs[i]; p.prob[i].ldw = d; p.prob[i].N = d;
+    p.prob[i].a_col = i * r; p.prob[i].kind = i;
+  }
+  p.a32 = cur().z; p.lda = 3 * r;
+  p.out16 = cur().q; p.ldo16 = d;
+  p.k_cache = kc; p.v_cache = vc; p.seqlens = seqlens; p.S_max = S_max; p.kv_rows = kv_rows;
+  p.HD = d; p.D = L->D;
+  p.rope_cos = L->rope_cos; p.rope_sin = L->rope_sin;
+  return gemv_launch(p, PRO_F32, EPI_QKV, MAP_ROPE, B, target_ctas(), s);
+}
+
+// Stages 4-9: output projection of the attention buffer, MLP, residuals.
+int decode_rest(const flashsvd_layer* L, bf16* x, int B, cudaStream_t s) {
+  const int d = L->d;
+  // 4-5) x = x + (att . U_o) . V_o
+  FSVD_TRY(decode_linear(cur().att, cb(L->o.U), cb(L->o.V), nullptr, x, x, B, d, L->o.r, d, nullptr, 0.f, s));
+  // 6-7) h = SiLU(gate) * up of rmsnorm(x)
+  FSVD_TRY(decode_gateup(x, cb(L->U_gu), cb(L->V_gu), cur().h, B, d, L->r_f, L->f,
+                         (const bf16*)L->norm2_g, L->norm_eps, s));
+  // 8-9) x = x + (h . U_dn) . V_dn
+  return decode_linear(cur().h, cb(L->down.U), cb(L->down.V), nullptr, x, x, B, L->f, L->down.r, d, nullptr, 0.f, s);
+}
+
 int layer_decode(const flashsvd_layer* L, bf16* x, bf16* kc, bf16* vc,
                  const int* seqlens, int B, int S_max, cudaStream_t s) {
   const int d = L->d, r = L->q.r;
-  const bool same_r = L->k.r == r && L->v.r == r;
   if (g_fused_decode && L->decode_pack && pack_shapes_ok(L) && cur().sm_count <= 148 &&
       decode_fused_supported(B, d, L->D, r, L->r_f)) {
     const DecodeLayerDesc D = decode_desc(L);
@@ -386,29 +427,8 @@ int layer_decode(const flashsvd_layer* L, bf16* x, bf16* kc, bf16* vc,
                                        cur().sm_count, s);
     if (st != FLASHSVD_ERR_UNSUPPORTED_SHAPE) return st;
   }
-  // 1) z_qkv = rmsnorm(x) . [U_q | U_k | U_v]
-  if (!same_r) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
-  {
-    const bf16* Us[3] = {(const bf16*)L->q.U, (const bf16*)L->k.U, (const bf16*)L->v.U};
-    const int Ns[3] = {r, r, r};
-    FSVD_TRY(decode_stage1(PRO_RMSNORM, x, d, (const bf16*)L->norm1_g, L->norm_eps, Us, Ns, 3, d, B, s));
-  }
-  // 2) q, k, v = z . V (RoPE on q, k; k, v appended at cache_seqlens[b])
-  {
-    GvParams p = gv_base();
-    p.K = r; p.nprob = 3;
-    const bf16* Vs[3] = {(const bf16*)L->q.V, (const bf16*)L->k.V, (const bf16*)L->v.V};
-    for (int i = 0; i < 3; ++i) {
-      p.prob[i].W = Vs[i]; p.prob[i].ldw = d; p.prob[i].N = d;
-      p.prob[i].a_col = i * r; p.prob[i].kind = i;
-    }
-    p.a32 = cur().z; p.lda = 3 * r;
-    p.out16 = cur().q; p.ldo16 = d;
-    p.k_cache = kc; p.v_cache = vc; p.seqlens = seqlens; p.S_max = S_max;
-    p.HD = d; p.D = L->D;
-    p.rope_cos = L->rope_cos; p.rope_sin = L->rope_sin;
-    FSVD_TRY(gemv_launch(p, PRO_F32, EPI_QKV, MAP_ROPE, B, target_ctas(), s));
-  }
+  // 1-2) q, k, v (k, v appended at cache_seqlens[b])
+  FSVD_TRY(decode_qkv(L, x, kc, vc, seqlens, B, S_max, 0, s));
   // 3) dense-KV attention over 0..pos
   FSVD_TRY(attn_fits(B, L->H, L->D, S_max));
   {
@@ -420,18 +440,56 @@ int layer_decode(const flashsvd_layer* L, bf16* x, bf16* kc, bf16* vc,
     a.part = cur().apart; a.counters = cur().acounters;
     FSVD_TRY(attn_decode_launch(a, target_ctas(), s));
   }
-  // 4-5) x = x + (att . U_o) . V_o
-  FSVD_TRY(decode_linear(cur().att, cb(L->o.U), cb(L->o.V), nullptr, x, x, B, d, L->o.r, d, nullptr, 0.f, s));
-  // 6-7) h = SiLU(gate) * up of rmsnorm(x)
-  FSVD_TRY(decode_gateup(x, cb(L->U_gu), cb(L->V_gu), cur().h, B, d, L->r_f, L->f,
-                         (const bf16*)L->norm2_g, L->norm_eps, s));
-  // 8-9) x = x + (h . U_dn) . V_dn
-  return decode_linear(cur().h, cb(L->down.U), cb(L->down.V), nullptr, x, x, B, L->f, L->down.r, d, nullptr, 0.f, s);
+  return decode_rest(L, x, B, s);
 }
+
+// Attention over the 8-bit cache in the workspace of this context.
+int kv8_attn(const bf16* q, const bf16* k_new, const bf16* v_new, const Kv8& c, const int* seqlens, float* weights,
+             int accumulate, bf16* out, int H, float scale_log2, cudaStream_t s) {
+  Kv8AttnParams a;
+  memset(&a, 0, sizeof(a));
+  a.q = q; a.k_new = k_new; a.v_new = v_new; a.c = c;
+  a.seqlens = seqlens; a.weights = weights; a.accumulate = accumulate; a.out = out;
+  a.H = H; a.scale_log2 = scale_log2;
+  a.part = cur().df_part; a.part_cap = kFusedPartFloats;
+  a.scores = cur().apart; a.scores_cap = (long long)cur().apart_elems;
+  a.counters = cur().acounters; a.counters_cap = kCountersN;
+  a.status = cur().status;
+  return kv8_attn_launch(a, cur().sm_count, s);
+}
+
+int weight_sums(const bf16* q, const bf16* k, float* weights, const int* lens, int B, int S, int H, int G, int D,
+                int S_max, int w_stride, int window, float scale_log2, cudaStream_t s) {
+  AttnSumsParams a;
+  memset(&a, 0, sizeof(a));
+  a.q = q; a.k = k; a.weights = weights; a.lens = lens;
+  a.B = B; a.S = S; a.H = H; a.G = G; a.D = D; a.S_max = S_max; a.w_stride = w_stride; a.window = window;
+  a.scale_log2 = scale_log2;
+  a.ws = cur().apart; a.ws_cap = (long long)cur().apart_elems;
+  a.counters = cur().acounters; a.counters_cap = kCountersN;
+  a.status = cur().status;
+  return attn_sums_launch(a, cur().sm_count, s);
+}
+
+// The decode layer over the 8-bit cache; k, v: [B x H*D] rows for the new token.
+int layer_decode_kv8(const flashsvd_layer* L, bf16* x, const Kv8& c, bf16* k, bf16* v, float* weights,
+                     const int* seqlens, const int* positions, int rope_rows, int B, cudaStream_t s) {
+  FSVD_TRY(decode_qkv(L, x, k, v, positions, B, rope_rows, 1, s));
+  FSVD_TRY(kv8_attn(cur().q, k, v, c, seqlens, weights, 1, cur().att, L->H,
+                    1.4426950408889634f / sqrtf((float)L->D), s));
+  return decode_rest(L, x, B, s);
+}
+
+// The prompt's rows into an 8-bit cache, and their weights (prefill layers).
+struct PrefillKv8 {
+  Kv8 cache;
+  float* weights;  // or null
+  int window;
+};
 
 // ------------------------------------------------------ layer: prefill ----
 int layer_prefill(const flashsvd_layer* L, bf16* x, bf16* kc, bf16* vc,
-                  int B, int S, int S_max, cudaStream_t s) {
+                  int B, int S, int S_max, const PrefillKv8* k8, cudaStream_t s) {
   const int d = L->d, M = B * S;
   FSVD_TRY(rmsnorm_launch(x, cb(L->norm1_g), cur().xn, M, d, L->norm_eps, s));
   const flashsvd_factor* F[3] = {&L->q, &L->k, &L->v};
@@ -444,7 +502,8 @@ int layer_prefill(const flashsvd_layer* L, bf16* x, bf16* kc, bf16* vc,
   // from the grouped stage 1, the attention kernel forms q = rope(z_q V_q)
   // itself, so q's stage 2 is not run and dense q is never materialised.
   // k and v still go through stage 2: decode reads them from the cache.
-  const bool fact_q = grouped && L->q.r % 64 == 0 && g_prefill_qf == 1;
+  // (The weights of an 8-bit cache's tokens are summed from dense q.)
+  const bool fact_q = grouped && L->q.r % 64 == 0 && g_prefill_qf == 1 && !(k8 && k8->weights);
   if (grouped && L->k.r == L->q.r && L->v.r == L->q.r) {
     FSVD_TRY(qkv_stage2_grouped(F, zg, fact_q ? 1 : 0, M, d, L->D, S, S_max, cur().q, kc, vc, L->rope_cos,
                                 L->rope_sin, s));
@@ -472,6 +531,12 @@ int layer_prefill(const flashsvd_layer* L, bf16* x, bf16* kc, bf16* vc,
     a.q = cur().q;
   }
   FSVD_TRY(attn_prefill_launch(a, s));
+  if (k8) {
+    FSVD_TRY(kv8_store_launch(kc, vc, k8->cache, nullptr, S, S_max, s));
+    if (k8->weights)
+      FSVD_TRY(weight_sums(cur().q, kc, k8->weights, nullptr, B, S, L->H, L->H, L->D, S_max, k8->cache.S_max,
+                           k8->window, a.scale_log2, s));
+  }
   {
     PfLinear p = pf_base(cur().att, d, L->o, M, d, d, x, d);
     p.resid = x; p.ldr = d;
@@ -1027,26 +1092,16 @@ int flashsvd_kv8_decode_attn(const flashsvd_bf16* q, const flashsvd_bf16* k_new,
                              const flashsvd_kv8* cache, const int32_t* cache_seqlens, float* weights,
                              int accumulate, flashsvd_bf16* out, int H, float scale, flashsvd_stream stream) {
   FSVD_TRY(need_init());
-  Kv8AttnParams a;
-  memset(&a, 0, sizeof(a));
-  FSVD_TRY(check_kv8(cache, &a.c));
+  Kv8 c;
+  FSVD_TRY(check_kv8(cache, &c));
   FSVD_TRY(check_ptr(q)); FSVD_TRY(check_ptr(out));
   if (!cache_seqlens || (k_new == nullptr) != (v_new == nullptr)) return FLASHSVD_ERR_INVALID_ARG;
   FSVD_TRY(check_opt_ptr(k_new)); FSVD_TRY(check_opt_ptr(v_new)); FSVD_TRY(check_opt_ptr(weights));
-  if (H <= 0 || H % a.c.G || !(scale > 0.f)) return FLASHSVD_ERR_INVALID_ARG;
-  if (H / a.c.G > 16) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
-  if (a.c.B == 0) return FLASHSVD_OK;
-  a.q = cb(q); a.k_new = cb(k_new); a.v_new = cb(v_new);
-  a.seqlens = cache_seqlens;
-  a.weights = weights; a.accumulate = accumulate != 0;
-  a.out = (bf16*)out;
-  a.H = H;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.part = cur().df_part; a.part_cap = kFusedPartFloats;
-  a.scores = cur().apart; a.scores_cap = (long long)cur().apart_elems;
-  a.counters = cur().acounters; a.counters_cap = kCountersN;
-  a.status = cur().status;
-  return kv8_attn_launch(a, cur().sm_count, stream);
+  if (H <= 0 || H % c.G || !(scale > 0.f)) return FLASHSVD_ERR_INVALID_ARG;
+  if (H / c.G > 16) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
+  if (c.B == 0) return FLASHSVD_OK;
+  return kv8_attn(cb(q), cb(k_new), cb(v_new), c, cache_seqlens, weights, accumulate != 0, (bf16*)out, H,
+                  scale * 1.4426950408889634f, stream);
 }
 
 int flashsvd_attn_weight_sums(const flashsvd_bf16* q, const flashsvd_bf16* k_cache, float* weights,
@@ -1059,15 +1114,8 @@ int flashsvd_attn_weight_sums(const flashsvd_bf16* q, const flashsvd_bf16* k_cac
     return FLASHSVD_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
   if (B == 0 || S == 0) return FLASHSVD_OK;
-  AttnSumsParams a;
-  memset(&a, 0, sizeof(a));
-  a.q = cb(q); a.k = cb(k_cache); a.weights = weights; a.lens = lens;
-  a.B = B; a.S = S; a.H = H; a.G = H_kv; a.D = D; a.S_max = S_max; a.w_stride = w_stride; a.window = window;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.ws = cur().apart; a.ws_cap = (long long)cur().apart_elems;
-  a.counters = cur().acounters; a.counters_cap = kCountersN;
-  a.status = cur().status;
-  return attn_sums_launch(a, cur().sm_count, stream);
+  return weight_sums(cb(q), cb(k_cache), weights, lens, B, S, H, H_kv, D, S_max, w_stride, window,
+                     scale * 1.4426950408889634f, stream);
 }
 
 int flashsvd_kv8_evict(const flashsvd_kv8* src, const flashsvd_kv8* dst, const float* weights_in,
@@ -1173,13 +1221,40 @@ int flashsvd_layer_forward(const flashsvd_layer* L, flashsvd_bf16* x_inout,
   }
   if (mode == FLASHSVD_PREFILL_CAUSAL) {
     if (L->kind != FLASHSVD_DECODER) return FLASHSVD_ERR_INVALID_ARG;
-    return layer_prefill(L, x, kc, vc, B, S, S_max, stream);
+    return layer_prefill(L, x, kc, vc, B, S, S_max, nullptr, stream);
   }
   if (mode == FLASHSVD_ENCODER_BIDIR) {
     if (L->kind != FLASHSVD_ENCODER) return FLASHSVD_ERR_INVALID_ARG;
     return layer_encoder(L, x, kc, vc, B, S, S_max, stream);
   }
   return FLASHSVD_ERR_INVALID_ARG;
+}
+
+int flashsvd_layer_forward_kv8(const flashsvd_layer* L, flashsvd_bf16* x_inout, const flashsvd_kv8* cache,
+                               flashsvd_bf16* k_rows, flashsvd_bf16* v_rows, float* weights, int window,
+                               const int32_t* cache_seqlens, const int32_t* positions, int rope_rows, int B,
+                               int S, int mode, flashsvd_stream stream) {
+  FSVD_TRY(need_init());
+  FSVD_TRY(check_layer(L));
+  Kv8 c;
+  FSVD_TRY(check_kv8(cache, &c));
+  FSVD_TRY(check_ptr(x_inout)); FSVD_TRY(check_ptr(k_rows)); FSVD_TRY(check_ptr(v_rows));
+  FSVD_TRY(check_opt_ptr(weights));
+  if (L->kind != FLASHSVD_DECODER || B < 0 || S < 0 || c.B != B || c.G != L->H || c.D != L->D || rope_rows < 1)
+    return FLASHSVD_ERR_INVALID_ARG;
+  if (B == 0 || S == 0) return FLASHSVD_OK;
+  bf16* x = (bf16*)x_inout;
+  if (mode == FLASHSVD_DECODE) {
+    if (S != 1 || !cache_seqlens) return FLASHSVD_ERR_INVALID_ARG;
+    if (B > DECODE_MAX_ROWS) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
+    return layer_decode_kv8(L, x, c, (bf16*)k_rows, (bf16*)v_rows, weights, cache_seqlens,
+                            positions ? positions : cache_seqlens, rope_rows, B, stream);
+  }
+  if (mode != FLASHSVD_PREFILL_CAUSAL || S > c.S_max || S > rope_rows || (weights && window < 1))
+    return FLASHSVD_ERR_INVALID_ARG;
+  FSVD_TRY(ensure_scratch(B * S, L->d, L->f));
+  const PrefillKv8 k8 = {c, weights, window};
+  return layer_prefill(L, x, (bf16*)k_rows, (bf16*)v_rows, B, S, S, &k8, stream);
 }
 
 int flashsvd_capture_begin(flashsvd_stream stream) {

@@ -328,7 +328,7 @@ gemv_splitk_kernel(const __grid_constant__ GvParams p) {
       }
       bf16* dst;
       if (P.kind == 0) dst = p.out16 + (long long)b * p.ldo16;
-      else dst = (P.kind == 1 ? p.k_cache : p.v_cache) + ((long long)b * p.S_max + pos) * p.HD;
+      else dst = (P.kind == 1 ? p.k_cache : p.v_cache) + (p.kv_rows ? b : (long long)b * p.S_max + pos) * p.HD;
       dst[glo] = f2bf(lo);
       dst[glo + half] = f2bf(hv);
     }

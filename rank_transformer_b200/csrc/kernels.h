@@ -43,6 +43,7 @@ struct GvParams {
   const bf16* resid; long long ldr;                 // EPI_BF16 (may be null)
   bf16* k_cache; bf16* v_cache; const int* seqlens; // EPI_QKV
   int S_max, HD, D;
+  int kv_rows;                                      // k, v go to row b of k_cache, v_cache [M x HD]; S_max rows of rotary tables
   const float* rope_cos; const float* rope_sin;     // [S_max x D/2]
   // workspace
   float* part; int* counters;

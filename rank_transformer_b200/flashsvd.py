@@ -116,6 +116,8 @@ _SIGS = {
     "flashsvd_greedy": ([_p, _p, _i, _i, _p], _i),
     "flashsvd_advance_seqlens": ([_p, _i, _p], _i),
     "flashsvd_layer_forward": ([C.POINTER(Layer), _p, _p, _p, _p, _i, _i, _i, _i, _p], _i),
+    "flashsvd_layer_forward_kv8": ([C.POINTER(Layer), _p, C.POINTER(Kv8), _p, _p, _p, _i, _p, _p, _i,
+                                    _i, _i, _i, _p], _i),
     "flashsvd_decode_graph_capture": ([C.POINTER(Layer), _p, _p, _p, _p, _i, _i, _p,
                                        C.POINTER(_p)], _i),
     "flashsvd_capture_begin": ([_p], _i),
@@ -376,6 +378,13 @@ def layer_forward(layer: Layer, x, k_cache, v_cache, cache_seqlens, B, S, S_max,
                   mode, stream=None):
     _call("flashsvd_layer_forward", C.byref(layer), ptr(x), ptr(k_cache),
           ptr(v_cache), ptr(cache_seqlens), B, S, S_max, mode, stream_handle(stream))
+
+
+def layer_forward_kv8(layer: Layer, x, cache, k_rows, v_rows, weights, window, cache_seqlens,
+                      positions, rope_rows, B, S, mode, stream=None):
+    _call("flashsvd_layer_forward_kv8", C.byref(layer), ptr(x), _kv8(cache), ptr(k_rows),
+          ptr(v_rows), ptr(weights), window, ptr(cache_seqlens), ptr(positions), rope_rows, B, S,
+          mode, stream_handle(stream))
 
 
 # --------------------------------------------------------------- graphs --

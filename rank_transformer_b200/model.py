@@ -13,6 +13,10 @@ Technical Summary, Methodology 4), with positions held in device memory.
 Without packs, decode replays one graph per layer over the per-stage
 kernels.
 
+With ``kv_format`` the decoder keeps an 8-bit key/value cache per layer
+(kv8.KV8Cache) and, with ``kv_keep``, drops the tokens that attention hardly
+used whenever the cache is full; see DecoderModel.
+
 ``EncoderModel``: BERT-shaped post-LN encoder with every linear factorized.
 """
 from __future__ import annotations
@@ -24,6 +28,7 @@ import torch
 
 from . import flashsvd as fs
 from . import synth
+from .kv8 import KV8Cache
 
 
 @dataclasses.dataclass
@@ -62,13 +67,33 @@ def _bf16_normal(shape, std, gen, device):
 
 class DecoderModel:
     def __init__(self, cfg: DecoderConfig, B: int, S_max: int, seed: int = 0,
-                 device: str = "cuda", weights=None, head=None, decode_pack: bool = True):
-        """``weights``: optional list of per-layer dicts of device bf16
+                 device: str = "cuda", weights=None, head=None, decode_pack: bool = True,
+                 kv_format: str | None = None, kv_keep: int | None = None, kv_recent: int = 0,
+                 kv_window: int = 64, max_positions: int | None = None):
+        """``kv_format`` ("int8" or "e4m3"): 8-bit key/value caches of S_max
+        tokens (a multiple of 64) instead of the bf16 ones; decode then runs
+        the per-stage kernels.  ``kv_keep``: when a cache is full, ``generate``
+        evicts every head's tokens down to this many, the ``kv_recent`` newest
+        and those with the largest accumulated attention weight (the prompt's
+        tokens start with their weight from its last ``kv_window`` queries).
+        Tokens keep the rotary positions they had; ``max_positions`` (default
+        S_max) bounds them.
+
+        ``weights``: optional list of per-layer dicts of device bf16
         tensors (U_q, V_q, ..., U_gu, V_gu, U_dn, V_dn, g1, g2); ``head``:
         optional dict with the device tensors emb [vocab x d], g_final [d]
         and W_lm [d x vocab].  Whatever is not given is random-initialised
         from ``seed``."""
         self.cfg, self.B, self.S_max, self.device = cfg, B, S_max, device
+        self.kv_format, self.kv_keep, self.kv_recent, self.kv_window = \
+            kv_format, kv_keep, kv_recent, kv_window
+        if kv_keep is not None and (kv_format is None or not 1 <= kv_keep < S_max
+                                    or not 0 <= kv_recent <= kv_keep):
+            raise ValueError("kv_keep needs a kv_format, 1 <= kv_keep < S_max and "
+                             "0 <= kv_recent <= kv_keep")
+        self.max_positions = S_max if max_positions is None else max_positions
+        if self.max_positions < S_max:
+            raise ValueError("max_positions is at least S_max")
         gen = torch.Generator(device=device)
         gen.manual_seed(seed)
         d, f = cfg.d, cfg.f
@@ -95,13 +120,27 @@ class DecoderModel:
             self.emb = _bf16_normal((cfg.vocab, d), 1.0, gen, device)
             self.g_final = torch.ones(d, dtype=torch.bfloat16, device=device)
             self.W_lm = _bf16_normal((d, cfg.vocab), d ** -0.5, gen, device)
-        self.rope_cos = torch.empty((S_max, cfg.D // 2), dtype=torch.float32, device=device)
+        self.rope_cos = torch.empty((self.max_positions, cfg.D // 2), dtype=torch.float32, device=device)
         self.rope_sin = torch.empty_like(self.rope_cos)
-        fs.rope_table(self.rope_cos, self.rope_sin, S_max, cfg.D, cfg.rope_base)
-        self.k_cache = [torch.zeros((B, S_max, cfg.H, cfg.D), dtype=torch.bfloat16, device=device)
-                        for _ in range(cfg.layers)]
-        self.v_cache = [torch.zeros_like(k) for k in self.k_cache]
+        fs.rope_table(self.rope_cos, self.rope_sin, self.max_positions, cfg.D, cfg.rope_base)
         self.seqlens = torch.zeros(B, dtype=torch.int32, device=device)
+        self.length = 0              # tokens in the cache, position of the next token (host)
+        self.position = 0
+        if kv_format is None:
+            self.k_cache = [torch.zeros((B, S_max, cfg.H, cfg.D), dtype=torch.bfloat16, device=device)
+                            for _ in range(cfg.layers)]
+            self.v_cache = [torch.zeros_like(k) for k in self.k_cache]
+        else:
+            self.kv8 = [KV8Cache(B, cfg.H, cfg.D, S_max, kv_format, device) for _ in range(cfg.layers)]
+            self.positions = torch.zeros(B, dtype=torch.int32, device=device)
+            self.k_row = torch.zeros((B, cfg.H, cfg.D), dtype=torch.bfloat16, device=device)
+            self.v_row = torch.zeros_like(self.k_row)
+            self.kv_rows = None      # the last prompt's key and value rows, all layers' scratch
+            self.kv_weights = [None] * cfg.layers
+            if kv_keep is not None:
+                self.kv_weights = [torch.zeros((B, cfg.H, S_max), device=device) for _ in range(cfg.layers)]
+                self.kept = torch.empty((B, cfg.H, kv_keep), dtype=torch.int32, device=device)
+            decode_pack = False
         self.x = torch.zeros((B, d), dtype=torch.bfloat16, device=device)
         self.xn = torch.zeros((B, d), dtype=torch.bfloat16, device=device)
         self.tokens = torch.zeros(B, dtype=torch.int32, device=device)
@@ -172,7 +211,14 @@ class DecoderModel:
         cfg = self.cfg
         x = torch.empty((B * S, cfg.d), dtype=torch.bfloat16, device=self.device)
         fs.embed(prompt.reshape(-1), self.emb, x, B * S, cfg.d, cfg.vocab, stream)
+        if self.kv_format is not None and (self.kv_rows is None or self.kv_rows.shape[1] != B * S):
+            self.kv_rows = torch.empty((2, B * S, cfg.d), dtype=torch.bfloat16, device=self.device)
         for i in range(cfg.layers):
+            if self.kv_format is not None:
+                fs.layer_forward_kv8(self.structs[i], x, self.kv8[i], self.kv_rows[0], self.kv_rows[1],
+                                     self.kv_weights[i], self.kv_window, None, None, self.max_positions, B, S,
+                                     fs.PREFILL_CAUSAL, stream)
+                continue
             fs.layer_forward(self.structs[i], x, self.k_cache[i], self.v_cache[i], None, B, S,
                              self.S_max, fs.PREFILL_CAUSAL, stream)
         last = x.view(B, S, cfg.d)[:, S - 1]
@@ -184,6 +230,9 @@ class DecoderModel:
             fs.dense_linear_f32(self.xn, self.W_lm, self.logits, B, cfg.d, cfg.vocab, stream)
         fs.greedy(self.logits, self.tokens, B, cfg.vocab, stream)
         self.seqlens.fill_(S)
+        if self.kv_format is not None:
+            self.positions.fill_(S)
+        self.length = self.position = S
         return x
 
     # ----------------------------------------------------------- decode --
@@ -198,8 +247,16 @@ class DecoderModel:
             fs.dense_linear_f32(self.xn, self.W_lm, self.logits, self.B, cfg.d, cfg.vocab, stream)
         fs.greedy(self.logits, self.tokens, self.B, cfg.vocab, stream)
         fs.advance_seqlens(self.seqlens, self.B, stream)
+        if self.kv_format is not None:
+            fs.advance_seqlens(self.positions, self.B, stream)
 
     def _layers_decode(self, stream):
+        if self.kv_format is not None:
+            for i in range(self.cfg.layers):
+                fs.layer_forward_kv8(self.structs[i], self.x, self.kv8[i], self.k_row, self.v_row,
+                                     self.kv_weights[i], 0, self.seqlens, self.positions,
+                                     self.max_positions, self.B, 1, fs.DECODE, stream)
+            return
         if self.plan is not None:
             self.plan.forward(self.x, self.seqlens, stream)
             return
@@ -212,17 +269,40 @@ class DecoderModel:
         fs.embed(self.tokens, self.emb, self.x, self.B, cfg.d, cfg.vocab, stream)
         self._layers_decode(stream)
         self._head(stream)
+        self.length += 1
+        self.position += 1
+
+    def evict(self, stream=None):
+        """Bring every head of every layer down to kv_keep tokens, in place
+        (a no-op while the cache holds no more).  The caches stay where they
+        are, so captured graphs go on with what is left."""
+        if self.kv_keep is None:
+            raise ValueError("the model was made without kv_keep")
+        for i, c in enumerate(self.kv8):
+            # every layer reads the lengths; the last one writes the new ones
+            out = self.seqlens if i == len(self.kv8) - 1 else None
+            fs.kv8_evict(c, c, self.kv_weights[i], self.kv_weights[i], self.seqlens, out, self.kept,
+                         self.kv_keep, self.kv_recent, stream)
+        self.length = min(self.length, self.kv_keep)
+
+    def _make_room(self, stream=None):
+        """Before a decode step of ``generate``: evict if the cache is full."""
+        if self.kv_keep is not None and self.length >= self.S_max:
+            self.evict(stream)
+        if self.length >= self.S_max or self.position >= self.max_positions:
+            raise ValueError(f"no room for another token: {self.length} of {self.S_max} cached, "
+                             f"position {self.position} of {self.max_positions}")
 
     def capture(self, stream, compose: bool = True):
         """Capture one graph per layer (plus the embedding and the head) and,
         with ``compose``, one graph for the whole step built from them."""
         cfg = self.cfg
-        if self.plan is not None:
-            # all layers are one launch: the step is one graph
+        if self.plan is not None or self.kv_format is not None:
+            # all layers are one launch, or read 8-bit caches: the step is one graph
             with torch.cuda.stream(stream):
                 fs.capture_begin(stream)
                 fs.embed(self.tokens, self.emb, self.x, self.B, cfg.d, cfg.vocab, stream)
-                self.plan.forward(self.x, self.seqlens, stream)
+                self._layers_decode(stream)
                 self._head(stream)
                 g = fs.capture_end(stream)
             self.graphs = [g]
@@ -248,6 +328,8 @@ class DecoderModel:
         else:
             for g in self.graphs:
                 g.replay(stream)
+        self.length += 1
+        self.position += 1
 
     def step_kernels(self) -> int:
         return sum(g.kernels for g in self.graphs)
@@ -266,7 +348,7 @@ class DecoderModel:
         the K/V history of every layer once, the new K/V rows, and the
         activations in and out (negligible)."""
         cfg = self.cfg
-        kv = 2 * cfg.layers * (context + 1) * cfg.d * 2 * self.B
+        kv = 2 * cfg.layers * (context + 1) * cfg.d * (1 if self.kv_format else 2) * self.B
         act = self.B * cfg.d * 2 * 2 * cfg.layers
         return self.weight_bytes() + kv + act
 
@@ -305,6 +387,8 @@ class DecoderModel:
         self.prefill(prompt, stream)
         for t in range(steps):
             gen[t].copy_(self.tokens, non_blocking=True)
+            if self.kv_format is not None:
+                self._make_room(stream)
             self.decode_step(stream)
         out = torch.empty((B, steps), dtype=torch.int32, pin_memory=True)
         out.copy_(gen.t(), non_blocking=True)
