@@ -66,6 +66,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+template <bool V>
+struct SuBool {
+  static constexpr bool value = V;
+};
+
 struct SuParams {
   const int* lens;
   float* weights;
@@ -213,6 +218,22 @@ __device__ __forceinline__ bool su_a_to_tmem(SuBars<D>* bars, const uint8_t* sme
   return ok;
 }
 
+// A thread's 64 scores from tensor memory; its warp's loads are done on return.
+__device__ __forceinline__ void su_scores(float (&s)[64], uint32_t addr, bool ok, float otherwise) {
+  if (ok) {
+    tc::fence_after_sync();
+    tc::tmem_ld32(addr, reinterpret_cast<uint32_t*>(s));
+    tc::tmem_ld32(addr + 32, reinterpret_cast<uint32_t*>(s + 32));
+    tc::tmem_ld_wait();
+    tc::reg_fence<64>(s);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 64; ++c) s[c] = otherwise;
+  }
+  tc::fence_before_sync();
+  __syncwarp();
+}
+
 // Persistent CTAs walk the items i G + c (odd rounds: i G + G - 1 - c) of a
 // list that begins with the longest ones, so that long and short ones pair up.
 // Every role walks the list by itself; an item with nothing to do is passed
@@ -356,49 +377,39 @@ attn_stats_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const int sb = k % L::NS, key0 = (w.t0 + k - t) * SU_RUN;
       ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->s_full + sb, (uint32_t)(k / L::NS) & 1u, &bars->abort_flag,
                                                        p.status));
-      float s[64];
-      if (ok) {
-        tc::fence_after_sync();
-        tc::tmem_ld32(tmem + lane_base + L::TM_S + sb * SU_RUN, reinterpret_cast<uint32_t*>(s));
-        tc::tmem_ld32(tmem + lane_base + L::TM_S + sb * SU_RUN + 32, reinterpret_cast<uint32_t*>(s + 32));
-        tc::tmem_ld_wait();
-        tc::reg_fence<64>(s);
-      } else {
+      // (two bodies, with the load in them: with one load and a branch around
+      // the mask alone every tile paid for the mask's selects)
+      auto tile = [&](auto diagonal) {
+        float s[64];
+        su_scores(s, tmem + lane_base + L::TM_S + sb * SU_RUN, ok, -INFINITY);
+        if (lane == 0) tc::mbar_arrive(bars->s_empty + sb);
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = -INFINITY;
-      }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bars->s_empty + sb);
-      // (a branch of its own for tiles on the diagonal: as selects in the one
-      // path, the mask cost every tile four instructions a score)
-      float mx;
-      if (__any_sync(0xffffffffu, key0 + 63 > q)) {
-        mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          s[c] = key0 + c > q ? -INFINITY : s[c];
-          mx = fmaxf(mx, s[c]);
+        for (int c = 0; c < 64; c += 2) {
+          if (diagonal.value) {
+            s[c] = key0 + c > q ? -INFINITY : s[c];
+            s[c + 1] = key0 + c + 1 > q ? -INFINITY : s[c + 1];
+          }
+          m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], s[c], s[c + 1]);
         }
-      } else {
-        float m4[4] = {s[0], s[1], s[2], s[3]};
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+        if (mx > m) {
+          l *= ex2f(m - mx);
+          m = mx;
+        }
+        const float e = m == -INFINITY ? 0.f : -m;
+        float a4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 4; c < 64; c += 2) m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], s[c], s[c + 1]);
-        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-      }
-      mx *= sc;
-      if (mx > m) {
-        l *= ex2f(m - mx);
-        m = mx;
-      }
-      const float e = m == -INFINITY ? 0.f : -m;
-      float a4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        fma2(s[c], s[c + 1], sc, e, e);
-        add2(a4[c & 2], a4[(c & 2) + 1], ex2f(s[c]), ex2f(s[c + 1]));
-      }
-      l += (a4[0] + a4[1]) + (a4[2] + a4[3]);
+        for (int c = 0; c < 64; c += 2) {
+          fma2(s[c], s[c + 1], sc, e, e);
+          add2(a4[c & 2], a4[(c & 2) + 1], ex2f(s[c]), ex2f(s[c + 1]));
+        }
+        l += (a4[0] + a4[1]) + (a4[2] + a4[3]);
+      };
+      if (__any_sync(0xffffffffu, key0 + 63 > q))
+        tile(SuBool<true>{});
+      else
+        tile(SuBool<false>{});
     }
     t += w.n;
     float2* x = xch + (done++ & 1) * 128 + row;  // (in turn: the last item's may still be read)
@@ -535,48 +546,35 @@ attn_sums_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                                                        p.status));
       ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->s_full + sb, (uint32_t)(k / L::NS) & 1u, &bars->abort_flag,
                                                        p.status));
-      float s[64];
-      if (ok) {
-        tc::fence_after_sync();
-        tc::tmem_ld32(tmem + lane_base + L::TM_S + sb * SU_RUN, reinterpret_cast<uint32_t*>(s));
-        tc::tmem_ld32(tmem + lane_base + L::TM_S + sb * SU_RUN + 32, reinterpret_cast<uint32_t*>(s + 32));
-        tc::tmem_ld_wait();
-        tc::reg_fence<64>(s);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = 0.f;
-      }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bars->s_empty + sb);
       const float4* ls = reinterpret_cast<const float4*>(smem + L::LSE + st * SU_RUN * 4);
-      float a4[4] = {0.f, 0.f, 0.f, 0.f};
-      if (q0 < key0 + SU_KEYS || q0 + SU_RUN > R.n) {
-        // queries before the key, and rows behind the sequence (whatever they hold)
-#pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 e = ls[c >> 2];
-          const float x[4] = {fmaf(s[c], sc, e.x), fmaf(s[c + 1], sc, e.y), fmaf(s[c + 2], sc, e.z),
-                              fmaf(s[c + 3], sc, e.w)};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float y = ex2f(x[i]);
-            a4[i] += q0 + c + i < key || q0 + c + i >= R.n ? 0.f : y;
-          }
-        }
-      } else {
+      auto tile = [&](auto edge) {
+        float s[64];
+        su_scores(s, tmem + lane_base + L::TM_S + sb * SU_RUN, ok, 0.f);
+        if (lane == 0) tc::mbar_arrive(bars->s_empty + sb);
+        float a4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < 64; c += 4) {
           const float4 e = ls[c >> 2];
           fma2(s[c], s[c + 1], sc, e.x, e.y);
           fma2(s[c + 2], s[c + 3], sc, e.z, e.w);
-          add2(a4[0], a4[1], ex2f(s[c]), ex2f(s[c + 1]));
-          add2(a4[2], a4[3], ex2f(s[c + 2]), ex2f(s[c + 3]));
+          float y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            y[i] = ex2f(s[c + i]);
+            if (edge.value) y[i] = q0 + c + i < key || q0 + c + i >= R.n ? 0.f : y[i];
+          }
+          add2(a4[0], a4[1], y[0], y[1]);
+          add2(a4[2], a4[3], y[2], y[3]);
         }
-      }
+        total += (a4[0] + a4[1]) + (a4[2] + a4[3]);
+      };
+      // edge: queries before the key, and rows behind the sequence (whatever they hold)
+      if (q0 < key0 + SU_KEYS || q0 + SU_RUN > R.n)
+        tile(SuBool<true>{});
+      else
+        tile(SuBool<false>{});
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bars->empty + st);
-      total += (a4[0] + a4[1]) + (a4[2] + a4[3]);
     }
     t += w.n;
     ++j;
