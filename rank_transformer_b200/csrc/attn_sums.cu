@@ -32,6 +32,7 @@ namespace {
 constexpr int SU_THREADS = 320;  // TMA warp, MMA warp, 8 softmax warps
 constexpr int SU_RUN = 64;       // query rows of a run
 constexpr int SU_KEYS = 128;     // keys of a tile
+constexpr int SU_MIN_TILES = 6;   // 64-key tiles of a split, at least
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -602,10 +603,15 @@ int launch_sums(const AttnSumsParams& a, int sm_count, cudaStream_t stream) {
   const long long pairs = (long long)a.B * a.G, heads = (long long)a.B * a.H;
   p.row_tiles = ceil_div(p.runs * p.rep, 2);
   const int key_tiles = ceil_div(a.S, SU_KEYS);
-  // With fewer row tiles than resident CTAs (two per SM) their keys are split.
+  // With fewer row tiles than resident CTAs (two per SM) their keys are split,
+  // SU_MIN_TILES 64-key tiles or more a part: joining parts costs about 4 us, as
+  // much as six tiles (300 tokens x 8 heads: five parts 17.2 us, one 13.8; last
+  // 64 of 4096 tokens, 8 heads, batch 2: parts of 2, 6 and 12 tiles 16.3, 17.5
+  // and 21.3).
   const long long tiles = pairs * p.row_tiles, slots = 2LL * sm_count;
-  long long splits = slots / tiles;
-  splits = splits < 1 || tiles > a.counters_cap ? 1 : (splits > 2 * key_tiles ? 2 * key_tiles : splits);
+  const long long parts = ceil_div(2 * key_tiles, SU_MIN_TILES);
+  long long splits = slots / tiles < parts ? slots / tiles : parts;
+  if (splits < 1 || tiles > a.counters_cap) splits = 1;
   p.splits = (int)splits;
   const long long lse = heads * p.runs * SU_RUN;
   const long long part = splits > 1 ? tiles * splits * 128 * 2 : 0;
