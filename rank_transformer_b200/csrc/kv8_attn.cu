@@ -244,13 +244,14 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const int end = r.pair0 + r.nblk <= u_end ? r.nblk - 1 : u_end - r.pair0;
     return r.nblk > 0 ? (end - r.j0) * (KV8_BLOCK / 16) : 0;
   };
+  const uint64_t once = tc::policy_evict_first();
   auto issue = [&](const KaPair& r, int s, int use) {
     const int row = (int)((((long long)r.b * G + r.g) * S_max + (long long)r.j0 * KV8_BLOCK) * D / 128) + s * (L::HALF / 128);
     const int st = use % NST;
     uint8_t* dst = ring + st * 2 * L::HALF;
     tc::mbar_expect_tx(bar + st, 2 * L::HALF);
-    tc::tma_load_2d(dst, &tmK, bar + st, 0, row);
-    tc::tma_load_2d(dst + L::HALF, &tmV, bar + st, 0, row);
+    tc::tma_load_2d_once(dst, &tmK, bar + st, 0, row, once);
+    tc::tma_load_2d_once(dst + L::HALF, &tmV, bar + st, 0, row, once);
   };
   auto issue_first = [&](const KaPair& r, int use) {
     const int n_t = tail_slices(r), n_c = code_slices(r);
