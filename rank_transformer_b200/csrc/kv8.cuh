@@ -30,12 +30,6 @@ __device__ __forceinline__ uint4 ld_once(const void* p) {
                : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint2 ld_once8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-
 // Exponent field of a bf16 magnitude (bits without sign) -> the block
 // exponent e.  amax = (1 + m / 128) 2^(E - 127):
 //   int8: amax <= 127 2^e   <=>  e >= E - 133, or E - 132 when 1 + m/128 > 127/64
