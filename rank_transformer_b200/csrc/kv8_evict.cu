@@ -82,6 +82,11 @@ __device__ __forceinline__ uint4 ld_cluster4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void st_cluster4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 // A cluster of `ctas` CTAs per pair, each with one stretch of the weights;
 // every thread keeps KPT consecutive ones in registers (a stretch longer than
 // a CTA's threads hold is walked in tiles, read again each time).  Three
@@ -95,6 +100,7 @@ kv8_select_kernel(const __grid_constant__ EvParams p) {
   constexpr int TILE = EV_SEL_THREADS * KPT, BPT = EV_BINS / EV_SEL_THREADS;
   static_assert(BPT == 4, "four digits a thread");
   __shared__ __align__(16) uint32_t hist[EV_BINS];
+  __shared__ uint4 s_share[EV_SEL_THREADS], s_all[EV_SEL_THREADS];
   __shared__ uint32_t s_scan[EV_SEL_THREADS / 32], s_res[2];
   __shared__ __align__(8) uint32_t s_tot[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -140,7 +146,6 @@ kv8_select_kernel(const __grid_constant__ EvParams p) {
   load(0);
 
   uint32_t prefix = 0, need = hk, total;
-  const uint32_t hist_at = tc::smem_u32(hist) + 4 * BPT * tid;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
@@ -154,16 +159,23 @@ kv8_select_kernel(const __grid_constant__ EvParams p) {
           atomicAdd(&hist[(keys[k] >> shift) & ((1u << bits) - 1u)], 1u);
     }
     if (ctas > 1) tc::cluster_sync(); else __syncthreads();
-    uint32_t d[BPT] = {0, 0, 0, 0};  // counts of digits 4 tid .. + 3
-#pragma unroll
-    for (int r0 = 0; r0 < EV_SEL_CTAS; r0 += 4) {
-      uint4 v[4];  // (loads in flight together: one takes about a microsecond)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        v[r] = r0 + r < ctas ? ld_cluster4(tc::mapa_shared(hist_at, r0 + r)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) { d[0] += v[r].x; d[1] += v[r].y; d[2] += v[r].z; d[3] += v[r].w; }
+    if (ctas > 1) {
+      // Each CTA adds up its share of the digits (of four) and hands the sums
+      // to all: one load and one store a thread, about a microsecond each
+      // (every CTA reading all the counts took eight loads and 5 us).
+      const int per = EV_SEL_THREADS / ctas, r = tid / per, q = tid - r * per;
+      s_share[tid] = ld_cluster4(tc::mapa_shared(tc::smem_u32(hist) + 16 * (rank * per + q), r));
+      __syncthreads();
+      uint4 v = make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < ctas; ++k) {
+        const uint4 o = s_share[k * per + q];
+        v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+      }
+      st_cluster4(tc::mapa_shared(tc::smem_u32(s_all) + 16 * (rank * per + q), r), v);
+      tc::cluster_sync();
     }
+    const uint4 counts = ctas > 1 ? s_all[tid] : *reinterpret_cast<const uint4*>(hist + BPT * tid);
+    const uint32_t d[BPT] = {counts.x, counts.y, counts.z, counts.w};  // of digits 4 tid .. + 3
     const uint32_t sum = d[0] + d[1] + d[2] + d[3];
     uint32_t above = block_before<true>(sum, s_scan, lane, warp, &total);
     if (above < need && above + sum >= need) {
@@ -176,7 +188,7 @@ kv8_select_kernel(const __grid_constant__ EvParams p) {
         above += d[k];
       }
     }
-    if (ctas > 1) tc::cluster_sync(); else __syncthreads();
+    __syncthreads();  // (the others' next sums come after the next cluster barrier)
     prefix = s_res[0];
     need = s_res[1];
   }
