@@ -99,8 +99,12 @@ __global__ void __launch_bounds__(EV_SEL_THREADS, 2)
 kv8_select_kernel(const __grid_constant__ EvParams p) {
   constexpr int TILE = EV_SEL_THREADS * KPT, BPT = EV_BINS / EV_SEL_THREADS;
   static_assert(BPT == 4, "four digits a thread");
-  __shared__ __align__(16) uint32_t hist[EV_BINS];
-  __shared__ uint4 s_share[EV_SEL_THREADS], s_all[EV_SEL_THREADS];
+  // the digits' counts of the stretch, a share of all, the sums; then kept offsets
+  __shared__ uint4 s_buf[4 * EV_SEL_THREADS];
+  static_assert(TILE * 2 <= sizeof(s_buf) && EV_BINS * 4 <= EV_SEL_THREADS * 16, "room of s_buf");
+  uint32_t* hist = reinterpret_cast<uint32_t*>(s_buf);
+  uint4* s_share = s_buf + EV_SEL_THREADS;
+  uint4* s_all = s_buf + 2 * EV_SEL_THREADS;
   __shared__ uint32_t s_scan[EV_SEL_THREADS / 32], s_res[2];
   __shared__ __align__(8) uint32_t s_tot[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -194,19 +198,22 @@ kv8_select_kernel(const __grid_constant__ EvParams p) {
   }
 
   // every key above `prefix`, and the first `need` equal to it
+  uint32_t before = 0;
+  auto count = [&]() {  // those of the tile in the threads before: above, and equal << 16 (a tile holds under 2^16 keys)
+    uint32_t mine = 0;
+#pragma unroll
+    for (int k = 0; k < KPT; ++k)
+      if (k < have) mine += keys[k] > prefix ? 1u : keys[k] == prefix ? 0x10000u : 0u;
+    before = block_before<false>(mine, s_scan, lane, warp, &total);
+  };
   uint32_t g = 0, e = 0;  // of those, in the stretches and tiles before
   if (ctas > 1) {
-    uint32_t mine = 0;
     uint32_t tg = 0, te = 0;
     for (int tile = 0; tile < tiles; ++tile) {
       if (tiles > 1) load(tile);
-#pragma unroll
-      for (int k = 0; k < KPT; ++k)
-        if (k < have) mine += keys[k] > prefix ? 1u : keys[k] == prefix ? 0x10000u : 0u;
-      block_before<false>(mine, s_scan, lane, warp, &total);  // (a tile holds under 2^16 keys)
+      count();
       __syncthreads();
       tg += total & 0xffffu; te += total >> 16;
-      mine = 0;
     }
     if (tid == 0) { s_tot[0] = tg; s_tot[1] = te; }
     tc::cluster_sync();
@@ -215,25 +222,27 @@ kv8_select_kernel(const __grid_constant__ EvParams p) {
     e = __reduce_add_sync(0xffffffffu, t.y);
     tc::cluster_sync();  // (no CTA leaves while its counts may be read)
   }
+  // A tile's kept offsets go to shared memory first and from there in order
+  // (written at once, each thread's to its own place, they took 10 us).
+  uint16_t* s_off = reinterpret_cast<uint16_t*>(s_buf);
   for (int tile = 0; tile < tiles; ++tile) {
     if (tiles > 1) load(tile);
-    uint32_t mine = 0;
-#pragma unroll
-    for (int k = 0; k < KPT; ++k)
-      if (k < have) mine += keys[k] > prefix ? 1u : keys[k] == prefix ? 0x10000u : 0u;
-    const uint32_t before = block_before<false>(mine, s_scan, lane, warp, &total);
+    if (tiles > 1 || ctas == 1) count();
+    const uint32_t base = g + min(e, need);
     uint32_t gk = g + (before & 0xffffu), ek = e + (before >> 16);
-    const int at = first + tile * TILE + tid * KPT;
 #pragma unroll
     for (int k = 0; k < KPT; ++k)
       if (k < have) {
         const bool gt = keys[k] > prefix, eq = keys[k] == prefix;
-        if (gt || (eq && ek < need)) kept[gk + min(ek, need)] = at + k;
+        if (gt || (eq && ek < need)) s_off[gk + min(ek, need) - base] = (uint16_t)(tid * KPT + k);
         gk += gt;
         ek += eq;
       }
     g += total & 0xffffu;
     e += total >> 16;
+    __syncthreads();
+    const int at = first + tile * TILE, found = (int)(g + min(e, need) - base);
+    for (int i = tid; i < found; i += EV_SEL_THREADS) kept[base + i] = at + s_off[i];
     __syncthreads();
   }
 }
