@@ -417,8 +417,9 @@ FLASHSVD_API int flashsvd_attn_weight_sums(const flashsvd_bf16* q, const flashsv
  * block with a smaller largest value gets finer codes, one with a larger
  * coarser ones).  Nothing beyond m is written.
  * dst may be src itself (every pointer of the two equal; weights_out then
- * is weights_in): eviction in place.  Otherwise no buffer of dst, and not
- * weights_out, may overlap src.  seqlens_out may be seqlens_in.
+ * is weights_in): eviction in place.  Otherwise a buffer of dst, or
+ * weights_out, that overlaps one of src, or weights_in, is refused
+ * (FLASHSVD_ERR_INVALID_ARG).  seqlens_out may be seqlens_in.
  * 1 <= keep <= dst S_max, keep <= src S_max, 0 <= recent <= keep; src and
  * dst of one format, B, H_kv and D. */
 FLASHSVD_API int flashsvd_kv8_evict(const flashsvd_kv8* src, const flashsvd_kv8* dst,

@@ -287,6 +287,27 @@ int check_kv8(const flashsvd_kv8* c, Kv8* out) {
   return FLASHSVD_OK;
 }
 
+// Whether a buffer of the two caches or of their weights overlaps one of the other's.
+bool kv8_overlap(const Kv8& a, const float* wa, const Kv8& b, const float* wb) {
+  struct Range { uintptr_t at, bytes; };
+  auto ranges = [](const Kv8& c, const float* w, Range* r) {
+    const uintptr_t pairs = (uintptr_t)c.B * c.G, rows = pairs * c.S_max;
+    for (int x = 0; x < 2; ++x) {
+      r[3 * x] = {(uintptr_t)c.codes[x], rows * c.D};
+      r[3 * x + 1] = {(uintptr_t)c.scale[x], rows / KV8_BLOCK * 4};
+      r[3 * x + 2] = {(uintptr_t)c.tail[x], pairs * KV8_BLOCK * c.D * 2};
+    }
+    r[6] = {(uintptr_t)w, rows * 4};
+  };
+  Range ra[7], rb[7];
+  ranges(a, wa, ra);
+  ranges(b, wb, rb);
+  for (const Range& x : ra)
+    for (const Range& y : rb)
+      if (x.at < y.at + y.bytes && y.at < x.at + x.bytes) return true;
+  return false;
+}
+
 PfLinear pf_base(const bf16* x, long long ldx, const flashsvd_factor& F, int M,
                  int d, int n, bf16* y, long long ldy) {
   PfLinear p;
@@ -1131,14 +1152,14 @@ int flashsvd_kv8_evict(const flashsvd_kv8* src, const flashsvd_kv8* dst, const f
     return FLASHSVD_ERR_INVALID_ARG;
   if (keep < 1 || keep > a.src.S_max || keep > a.dst.S_max || recent < 0 || recent > keep)
     return FLASHSVD_ERR_INVALID_ARG;
-  // in place: all of src's buffers, or none of them
+  // in place: all of src's buffers, or apart from all of them
   int same = weights_in == weights_out;
   for (int x = 0; x < 2; ++x)
     same += (a.src.codes[x] == a.dst.codes[x]) + (a.src.scale[x] == a.dst.scale[x]) +
             (a.src.tail[x] == a.dst.tail[x]);
-  if (same != 0 && same != 7) return FLASHSVD_ERR_INVALID_ARG;
   if (same == 7 && a.src.S_max != a.dst.S_max) return FLASHSVD_ERR_INVALID_ARG;
   if (a.src.B == 0) return FLASHSVD_OK;
+  if (same != 7 && kv8_overlap(a.src, weights_in, a.dst, weights_out)) return FLASHSVD_ERR_INVALID_ARG;
   a.w_in = weights_in; a.w_out = weights_out;
   a.n_in = seqlens_in; a.n_out = seqlens_out; a.kept = kept;
   a.keep = keep; a.recent = recent; a.in_place = same == 7;

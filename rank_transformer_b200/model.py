@@ -212,6 +212,8 @@ class DecoderModel:
         x = torch.empty((B * S, cfg.d), dtype=torch.bfloat16, device=self.device)
         fs.embed(prompt.reshape(-1), self.emb, x, B * S, cfg.d, cfg.vocab, stream)
         if self.kv_format is not None and (self.kv_rows is None or self.kv_rows.shape[1] != B * S):
+            if self.kv_rows is not None and stream is not None:
+                self.kv_rows.record_stream(stream)  # an earlier prompt's work may still use it
             self.kv_rows = torch.empty((2, B * S, cfg.d), dtype=torch.bfloat16, device=self.device)
         for i in range(cfg.layers):
             if self.kv_format is not None:
