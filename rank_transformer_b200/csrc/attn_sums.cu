@@ -220,17 +220,14 @@ __device__ __forceinline__ bool su_a_to_tmem(SuBars<D>* bars, const uint8_t* sme
 }
 
 // A thread's 64 scores from tensor memory; its warp's loads are done on return.
-__device__ __forceinline__ void su_scores(float (&s)[64], uint32_t addr, bool ok, float otherwise) {
-  if (ok) {
-    tc::fence_after_sync();
-    tc::tmem_ld32(addr, reinterpret_cast<uint32_t*>(s));
-    tc::tmem_ld32(addr + 32, reinterpret_cast<uint32_t*>(s + 32));
-    tc::tmem_ld_wait();
-    tc::reg_fence<64>(s);
-  } else {
-#pragma unroll
-    for (int c = 0; c < 64; ++c) s[c] = otherwise;
-  }
+// (After a failed wait too, whatever is there: a second source for the scores
+// would cost a move for each.)
+__device__ __forceinline__ void su_scores(float (&s)[64], uint32_t addr) {
+  tc::fence_after_sync();
+  tc::tmem_ld32(addr, reinterpret_cast<uint32_t*>(s));
+  tc::tmem_ld32(addr + 32, reinterpret_cast<uint32_t*>(s + 32));
+  tc::tmem_ld_wait();
+  tc::reg_fence<64>(s);
   tc::fence_before_sync();
   __syncwarp();
 }
@@ -382,7 +379,7 @@ attn_stats_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       // the mask alone every tile paid for the mask's selects)
       auto tile = [&](auto diagonal) {
         float s[64];
-        su_scores(s, tmem + lane_base + L::TM_S + sb * SU_RUN, ok, -INFINITY);
+        su_scores(s, tmem + lane_base + L::TM_S + sb * SU_RUN);
         if (lane == 0) tc::mbar_arrive(bars->s_empty + sb);
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -550,7 +547,7 @@ attn_sums_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const float4* ls = reinterpret_cast<const float4*>(smem + L::LSE + st * SU_RUN * 4);
       auto tile = [&](auto edge) {
         float s[64];
-        su_scores(s, tmem + lane_base + L::TM_S + sb * SU_RUN, ok, 0.f);
+        su_scores(s, tmem + lane_base + L::TM_S + sb * SU_RUN);
         if (lane == 0) tc::mbar_arrive(bars->s_empty + sb);
         float a4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
