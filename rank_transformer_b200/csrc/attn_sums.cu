@@ -3,24 +3,43 @@
 //     weights[b, g, j] = sum_{h in group g} sum_{i in window, i >= j}
 //                        2^(x_hij - lse_hi),   x = log2(e) scale q_hi . k_gj.
 //
-// Launch 1 (stats): lse_hi = log2 sum_{j <= i} 2^(x_hij).  A CTA takes 128
+// Launch 1 (stats): lse_hi = log2 sum_{j <= i} 2^(x_hij).  An item is 128
 // query rows of one KV head (two runs of 64: consecutive ones of a head, or
-// two heads of the group, which share the keys) and walks 128-key tiles:
-// S = Q K^T on the tensor cores, one running (max, sum) per row and half
-// tile.  With few row tiles the keys are split over CTAs and the CTA that
+// two heads of the group, which share the keys); it walks 64-key tiles: S =
+// Q K^T on the tensor cores, one running (max, sum) per row and group of
+// warps.  With few row tiles the keys are split over items, and the CTA that
 // finishes a row tile last joins the parts in split order.
-// Launch 2 (sums): a CTA keeps 128 keys and walks the 64-row runs of
-// queries that see them, S^T = K Q^T: a thread owns a key (half of a run's
-// queries each) and adds up 2^(x - lse) in fp32, one partial sum a run.  No
-// atomics: the order of every sum is fixed.
+// Launch 2 (sums): an item is 128 keys; it walks the 64-row runs of queries
+// that see them, S^T = K Q^T: a thread owns a key and adds up 2^(x - lse) in
+// fp32, one partial sum a run.  No atomics: the order of every sum is fixed.
 //
 // The scores are computed twice (2 D flops each) because keeping them would
-// write and read 4 bytes per (query, key, head).  Both launches are bound by
-// the special-function unit (one exponential per score; 16 per clock and SM
-// against 4096 multiply-adds, that is D = 128 scores in half the time).
-// 96 KB of shared memory and 256 tensor-memory columns per CTA let two CTAs
-// share an SM, so that one's waits are filled by the other.  Every wait is
-// bounded.
+// write and read 4 bytes per (query, key, head): at 2048 tokens x 32 heads
+// 268 MB each way, 80 us.  Both launches are bound by the special-function
+// unit, one exponential per score: 16 per clock and SM, 512 clocks for a 128 x
+// 64 tile, which its products (N = 64 runs at half the tensor rate) take too
+// at D = 128.
+//
+// Persistent CTAs, two per SM, so that one's waits are filled by the other (98
+// KB of shared memory, 256 tensor-memory columns, 96 registers a thread): a
+// TMA warp, an MMA warp, and two groups of four softmax warps that take the
+// tiles in turn.  2048 tokens x 32 heads / the last 64 of 16000 tokens, 32
+// heads, batch 2, both launches: both operands in shared memory and an item a
+// CTA 78 / 87 us; the stationary one in tensor memory, packed arithmetic 63 /
+// 74; persistent CTAs that load the next item's operand meanwhile 63 / 64;
+// masked tiles in a body of their own, no second source for the scores 60.5 /
+// 61 (the exponentials alone: 30 / 29).  4096 tokens: 180 us (119).
+//
+// Not faster: one CTA per SM with 128 x 128 tiles and a quarter of the
+// exponentials on the FMA pipe (201 us at 4096 tokens), 256 stationary rows
+// (207: half the traffic from L2), 128 x 128 tiles in two CTAs with one S
+// buffer (190), the same with the next item's operand in tensor memory ahead
+// of time (191).  Without the exponentials 4096 tokens take 159 us, without
+// seven eighths of the products 187, without both 120: the chain of waits,
+// tensor-memory loads and hand-offs of a tile (900 clocks), the exponentials
+// and the products each fill most of the time, and four warps per scheduler,
+// all that registers allow, overlap them to 0.65 of the exponentials' rate.
+// Every wait is bounded.
 #include <cstring>
 
 #include "kernels.h"

@@ -26,6 +26,20 @@
 // scaled by a power of two), the probabilities are rounded to half after
 // scaling by 2^15, so that they keep 11 bits down to 2^-29 and vanish only
 // below 2^-40 of the largest; l is summed from the unrounded ones.
+//
+// Bound by HBM where histories are long: 32 rows of up to 8191 tokens, 8 KV
+// heads of 128, take 55-58 us (46 for the bytes), 4 rows of 131071 tokens
+// without weights 164 us (163).  What it took there: rings of TMA loads in
+// place of loads by the threads, conflict-free reads, the split weighted by
+// pair (KA_PAIR_COST), and codes that leave the L2 first (61 -> 55 us, and
+// 108 -> 101 for two of the long rows with scores: the scores stay in the L2
+// for the second launch).  With weights the long rows take 246 us: the scores
+// are 134 MB, written and read (24 + 32 us), and the workspace holds two rows'
+// at a time, so there are two pairs of launches.  (Token-major scores, half
+// the store instructions: the attention took the same time and the second
+// launch twice as long, 33 us.)  2048 tokens of one sequence (32 heads) take
+// 13 us for 2.6 us of bytes: launch, first loads, the join of the warps and
+// of the CTAs follow one another.
 #include "kv8.cuh"
 #include "tc.cuh"
 
@@ -708,7 +722,10 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 }
 
 // weights[b, g, j] (+)= sum over the group's heads of 2^(x_j - M) / l, for
-// j = 0..pos; with `fresh` the entry of the token just appended is set.
+// j = 0..pos; with `fresh` the entry of the token just appended is set.  A
+// launch of its own, because M and l are known only once every CTA of a pair
+// is done; bound by memory (two rows of 131071 tokens, 64 heads: 84 MB, partly
+// from the L2, in 16 us).
 struct KwParams {
   const float* scores; const float* ml;
   const int* seqlens;
