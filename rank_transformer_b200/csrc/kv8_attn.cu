@@ -49,8 +49,14 @@ namespace {
 constexpr int KA_WARPS = 8;
 constexpr int KA_THREADS = 32 * KA_WARPS;
 constexpr int KA_MAX_WORKERS = 512;  // partials of one pair that the joining CTA has room for
-constexpr int KA_PAIR_COST = 12;   // what a pair costs beside its blocks, in blocks (work split)
-constexpr int KA_MIN_UNITS = 4;    // least units worth a CTA of their own
+// What a pair costs beside its blocks, in blocks (work split): joins, the
+// append and the first loads.  (64 rows of up to 600 tokens x 8 heads: 40 us
+// with 0, 23.7 with 12; 32 rows of up to 8191: 58 and 52.)
+constexpr int KA_PAIR_COST = 12;
+// Least units worth a CTA of their own (4 heads x 1000 tokens / 32 x 500: 1, 2,
+// 4 and 8 units 8.4, 8.8, 9.4, 10.9 / 10.4, 10.5, 11.5, 12.2 us; with 2 the two
+// blocks of a 100-token history still stay together).
+constexpr int KA_MIN_UNITS = 2;
 constexpr float KA_PSHIFT = 15.f;  // probabilities carry a factor 2^15 (it cancels in O / l)
 
 __device__ __forceinline__ float ex2(float x) {
