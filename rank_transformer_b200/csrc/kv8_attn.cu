@@ -581,9 +581,15 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       // the CTA that is last to leave a partial will join them, after its own
       // work (a CTA leaves at most two)
       const int nc = worker_of(pair0 + nblk - 1) - worker_of(pair0) + 1;
-      __threadfence();
+      // (the barrier orders the other threads' stores before thread 0's fence)
       __syncthreads();
-      if (tid == 0 && atomicAdd(p.counters + pair, 1) == nc - 1) s_join[u_begin < pair0 ? 1 : 0] = cur;
+      if (tid == 0) {
+        __threadfence();
+        if (atomicAdd(p.counters + pair, 1) == nc - 1) {
+          __threadfence();
+          s_join[u_begin < pair0 ? 1 : 0] = cur;
+        }
+      }
     }
 
     // ---- append: the new rows into the tail, a completed block into the codes ----
@@ -635,7 +641,6 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const int w0 = worker_of(pair0), nc = worker_of(pair0 + nblk - 1) - w0 + 1;
     const int late = first_of(w0) < pair0 ? 1 : 0;  // the pair is the last one of its first worker
     auto slot_of = [&](int k) { return p.part + (long long)(2 * (w0 + k) + (k == 0 ? late : 0)) * L::SLOT; };
-    __threadfence();
     float* fac = s_o;                         // [nc][HP] factors
     float* red = s_o + ((nc * HP + 3) & ~3);  // [groups][rep * D] sums
     // vectors of four sums; with few of them, groups of threads share the
