@@ -123,26 +123,34 @@ __device__ __forceinline__ void kv8_decode16h(const uint4& c, __half2* h) {
 // the format's limit by the choice of e.  A shift below -20 rounds every code
 // to zero, as -20 does.  In half precision the product is exact wherever the
 // result is not zero, and adding 1.5 * 2^10 in the same instruction rounds it
-// to an integer whose two's complement is the low byte (int8).
+// to an integer whose two's complement is the low byte (int8).  A code of 1
+// passes the int8 limit at 7, one of 2^-9 the e4m3 limit at 18: larger shifts
+// occur with zero codes alone, and those above 15, which half precision does
+// not hold, go in two steps.
 template <bool E4M3>
-__device__ __forceinline__ uint4 kv8_rescale16(const __half2* h, int shift) {
-  // (a shift above 14 occurs only with zero codes: a code of 1 or 2^-9 would
-  // pass the limit at 7 or 18, so e4m3 goes in two steps)
-  shift = shift < -20 ? -20 : (shift > 24 ? 24 : shift);
-  const int s1 = shift / 2, s2 = shift - s1;
-  const __half2 f1 = __float2half2_rn(exp2i(s1)), f2 = __float2half2_rn(exp2i(s2));
+__device__ __forceinline__ uint4 kv8_rescale16(__half2* h, int shift) {
+  shift = shift < -20 ? -20 : shift;
+  if (shift > 15) {
+    if (E4M3) {
+      const __half2 f = __float2half2_rn(exp2i((shift > 24 ? 24 : shift) - 15));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = __hmul2(h[i], f);
+    }
+    shift = 15;
+  }
+  const __half2 f = __float2half2_rn(exp2i(shift));
   uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (E4M3) {
-      const __half2 x = __hmul2(__hmul2(h[2 * i], f1), f2), y = __hmul2(__hmul2(h[2 * i + 1], f1), f2);
+      const __half2 x = __hmul2(h[2 * i], f), y = __hmul2(h[2 * i + 1], f);
       uint16_t lo, hi;
       asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
       asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(*reinterpret_cast<const uint32_t*>(&y)));
       r[i] = (uint32_t)lo | ((uint32_t)hi << 16);
     } else {
       const __half2 c = __float2half2_rn(1536.f);
-      const __half2 x = __hfma2(__hmul2(h[2 * i], f1), f2, c), y = __hfma2(__hmul2(h[2 * i + 1], f1), f2, c);
+      const __half2 x = __hfma2(h[2 * i], f, c), y = __hfma2(h[2 * i + 1], f, c);
       r[i] = __byte_perm(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y), 0x6420);
     }
   }

@@ -313,12 +313,12 @@ kv8_move_kernel(const __grid_constant__ EvParams p) {
         const int u = t + 128 * k, r = s_idx[u / UPR], col = (u % UPR) * 16;
         a[k] = c[k] = make_uint4(0, 0, 0, 0);
         sc[k] = -1.f;  // bf16 already
-        if (r >= 0 && r / KV8_BLOCK == last) {
+        if (r >= 0 && (int)((uint32_t)r / KV8_BLOCK) == last) {
           a[k] = ld_once(stail + (r % KV8_BLOCK) * D + col);
           c[k] = ld_once(stail + (r % KV8_BLOCK) * D + col + 8);
         } else if (r >= 0) {
           a[k] = ld_once(codes + (long long)r * D + col);
-          sc[k] = scale[r / KV8_BLOCK];
+          sc[k] = scale[(uint32_t)r / KV8_BLOCK];
         }
       }
       if (tid < rows) wv = p.w_in[(long long)pair * p.src.S_max + s_idx[tid]];
