@@ -8,13 +8,16 @@
 // per kept 64-token block gathers its rows into registers, finds their new
 // scale and writes codes, scale, weights and, for the newest block, the tail.
 //
-// 4 rows x 8 heads of 131072 tokens down to 32768 take 141 us against 86 for
+// 4 rows x 8 heads of 131072 tokens down to 32768 take 139 us against 86 for
 // the bytes: about 30 for the selection (7 until the weights are there, 5 to 6
 // for each of three rounds of counting, summing over the cluster and picking
-// the digit, the rest counting again and writing the indices), 111 for the
-// moves, whose rows of 128 bytes lie scattered (4.8 TB/s; a hint that they
-// leave the L2 first changed nothing).  2048 tokens of 32 heads down to 1024:
-// 12.4 us, two launches of a few us.
+// the digit, the rest counting again and writing the indices), 109 for the
+// moves, whose rows of 128 bytes lie scattered: 4.9 TB/s.  With 2, 3, 4 and
+// (spilling) 5 CTAs an SM the whole took 190, 160, 140 and 148 us; rows copied
+// to shared memory an item ahead 138, with numbers and indices two items ahead
+// 161; only codes held in registers, decoded twice, 5 CTAs 137; stores that
+// leave the L2 first 135 to 138, and what reads the cache next would miss.
+// 2048 tokens of 32 heads down to 1024: 12.4 us, two launches of a few us.
 //
 // In place, a kept row moves to a lower or equal index, so a CTA may write
 // block i only after the CTAs of lower blocks have loaded their rows from
@@ -298,7 +301,7 @@ kv8_move_kernel(const __grid_constant__ EvParams p) {
     // power of two, rounded, in one or two instructions a pair.  Otherwise
     // (the source's newest block, which is in its tail, or the destination's)
     // they become bf16.  (All of them as bf16 took 12 instructions an element
-    // and bound the kernel: 132 us, now 111, for 32 x 32768 rows of 128.)
+    // and bound the kernel: 132 us, then 111, for 32 x 32768 rows of 128.)
     const int last = (n - 1) / KV8_BLOCK;  // the source's newest block: in its tail
     const bool codes_only = row0 + KV8_BLOCK < m && s_idx[KV8_BLOCK - 1] / KV8_BLOCK < last;
     uint4 a[PER], c[PER];
