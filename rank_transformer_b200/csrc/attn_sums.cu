@@ -34,7 +34,7 @@
 // exponentials on the FMA pipe (201 us at 4096 tokens), 256 stationary rows
 // (207: half the traffic from L2), 128 x 128 tiles in two CTAs with one S
 // buffer (190), the same with the next item's operand in tensor memory ahead
-// of time (191).  Without the exponentials 4096 tokens take 159 us, without
+// of time (191), and with the next tile's scores loaded ahead too (203).  Without the exponentials 4096 tokens take 159 us, without
 // seven eighths of the products 187, without both 120: the chain of waits,
 // tensor-memory loads and hand-offs of a tile (900 clocks), the exponentials
 // and the products each fill most of the time, and four warps per scheduler,
