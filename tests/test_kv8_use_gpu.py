@@ -5,7 +5,10 @@ for bit: the operators have no atomics in their sums, so equal inputs and an
 equal work split give equal results."""
 import threading
 
+import numpy as np
 import pytest
+
+from oracle import flashsvd_oracle as oracle
 
 pytestmark = pytest.mark.gpu
 
@@ -187,6 +190,43 @@ def test_batch_cut_by_the_workspace(fs):
         # the probabilities of 16 heads; the appended token's are set, the others added to 2
         total = w[b, :, :n[b] + 1].double().sum() - 2.0 * n[b]
         assert abs(total - rep) < 1e-3  # 300 entries near 2, half a step of fp32 (2^-23) each, and 2^-20 a head
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_evict_scales_far_apart(fs, fmt, D):
+    """Blocks whose scale was set by a row that goes: the codes of the others
+    move by every power of two, up to where none is left, next to codes of
+    blocks whose scale hardly changes, and back down again."""
+    from tests.test_kv8_gpu import _bf16, _cache, _check_cache, _dev, _host
+    G, n, keep = 26, 256, 150
+    rng = np.random.default_rng(11)
+    x = [rng.standard_normal((1, n, G, D)) * 2.0 ** rng.integers(-3, 1, size=(1, n, G, D)) for _ in range(2)]
+    for g in range(G):
+        for blk, gap in enumerate((g, 7 * g % G, 25 - g)):
+            for t in x:
+                t[0, 64 * blk, g] = 2.0 ** gap * (1 + rng.random(D))
+    k, v = (_bf16(t) for t in x)
+    w = np.ones((1, G, 256), np.float32)
+    w[:, :, [0, 64, 128]] = 0.0
+    w[:, :, 153:] = 0.5
+    idx = oracle.evict_kept(w[0, 0].astype(np.float64), keep, 0)
+    assert not set(idx) & {0, 64, 128} and len(idx) == keep
+    for in_place in (False, True):
+        src = _cache(fs, 1, G, D, n, fmt)
+        fs.kv8_store(_dev(k), _dev(v), src, None, n, n)
+        dst = src if in_place else _cache(fs, 1, G, D, n, fmt, 0x11)
+        before = _host(dst)
+        wd = torch.from_numpy(w.copy()).cuda()
+        nd = torch.tensor([n], dtype=torch.int32, device="cuda")
+        kept = torch.zeros((1, G, keep), dtype=torch.int32, device="cuda")
+        fs.kv8_evict(src, dst, wd, wd if in_place else torch.zeros_like(wd), nd, None, kept, keep, 0)
+        torch.cuda.synchronize()
+        fs.check_device_status()
+        host = _host(dst)
+        for g in range(G):
+            for i, t in enumerate((k, v)):
+                _check_cache(host, before, i, 0, g, oracle.kv8_rows(t[0, :, g], fmt)[idx], fmt)
 
 
 def test_refusals(fs):
