@@ -28,7 +28,8 @@
 // CTA 78 / 87 us; the stationary one in tensor memory, packed arithmetic 63 /
 // 74; persistent CTAs that load the next item's operand meanwhile 63 / 64;
 // masked tiles in a body of their own, no second source for the scores 60.5 /
-// 61 (the exponentials alone: 30 / 29).  4096 tokens: 180 us (119).
+// 61; the second launch waiting for the statistics alone 59 / 59 (the
+// exponentials alone: 30 / 29).  4096 tokens: 180 us (119).
 //
 // Not faster: one CTA per SM with 128 x 128 tiles and a quarter of the
 // exponentials on the FMA pipe (201 us at 4096 tokens), 256 stationary rows
@@ -156,8 +157,6 @@ __device__ __forceinline__ uint32_t su_begin(SuBars<D>* bars, int readers, int w
   }
   __syncthreads();
   tc::fence_after_sync();
-  pdl_launch_dependents();
-  pdl_wait();
   return bars->tmem;
 }
 template <int D>
@@ -326,6 +325,10 @@ attn_stats_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   float2* xch = reinterpret_cast<float2*>(smem + L::XCH);  // [2][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t tmem = su_begin<D>(bars, 1, warp);
+  // q and k are there once this returns: the second launch, which can start
+  // now, reads them without waiting, and waits for the statistics alone
+  pdl_wait();
+  pdl_launch_dependents();
   const int items = p.B * p.G * p.row_tiles * p.splits;
 
   if (warp == 0) {
@@ -486,6 +489,7 @@ attn_sums_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   float* xch = reinterpret_cast<float*>(smem + L::XCH);  // [2][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t tmem = su_begin<D>(bars, 5, warp);      // the MMA and the four warps that read the lse
+  pdl_launch_dependents();
 
   const int items = p.B * p.G * ((p.S + SU_KEYS - 1) / SU_KEYS);
 
@@ -512,6 +516,7 @@ attn_sums_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           for (int kb = 0; kb < L::KB; ++kb)
             tc::tma_load_2d(smem + L::RING + (st * L::KB + kb) * L::RUN_B, &tmQ, bars->full + st, head * D + 64 * kb,
                             it.b * p.S + R.lo + run * SU_RUN);
+          if (k == 0) pdl_wait();  // for the statistics
           const float* src = p.lse + ((long long)(it.b * p.H + head) * p.runs + run) * SU_RUN;
           asm volatile(
               "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -601,6 +606,7 @@ attn_sums_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     if (grp == 0 && ok && key < R.n) p.weights[(long long)it.pair * p.w_stride + key] = total + *x;
     }  // items
   }
+  pdl_wait();  // (a CTA without items too: what follows this launch takes the one before it for done)
   su_end<D>(bars, tmem, warp, lane);
 }
 
