@@ -229,6 +229,35 @@ def test_evict_scales_far_apart(fs, fmt, D):
                 _check_cache(host, before, i, 0, g, oracle.kv8_rows(t[0, :, g], fmt)[idx], fmt)
 
 
+@pytest.mark.parametrize("B,S,G,rep,D,window,lens", [
+    (2, 2100, 2, 3, 64, 40, [2100, 130]),      # 7 parts a row tile; most of the short row's are empty
+    (1, 1500, 1, 1, 128, 1500, None),          # parts in front of, on and behind the diagonal
+    (3, 1025, 1, 2, 64, 97, [1, 0, 1025]),
+    (1, 4500, 1, 1, 128, 1, [4437]),
+])
+def test_weight_sums_in_parts(fs, B, S, G, rep, D, window, lens):
+    """Few rows of many keys: the statistics' keys are cut into parts."""
+    from tests.test_kv8_gpu import _bf16, _dev, _sums_bound
+    rng = np.random.default_rng(S)
+    H, scale = G * rep, D ** -0.5
+    q, k = _bf16(1.5 * rng.standard_normal((B, S, H, D))), _bf16(rng.standard_normal((B, S, G, D)))
+    n = lens or [S] * B
+    for b in range(B):
+        q[b, n[b]:], k[b, n[b]:] = np.nan, np.inf
+    w = torch.full((B, G, S), 7.0, device="cuda")
+    dl = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    fs.attn_weight_sums(_dev(q), _dev(k), w, dl, B, S, H, G, D, S, S, window, scale)
+    torch.cuda.synchronize()
+    fs.check_device_status()
+    got = w.double().cpu().numpy()
+    for b in range(B):
+        assert (got[b, :, n[b]:] == 7.0).all()
+        for g in range(G if n[b] else 0):
+            qq, kk = q[b, :n[b], g * rep:(g + 1) * rep], k[b, :n[b], g]
+            want = oracle.attn_weight_sums(qq, kk, window, scale)
+            assert np.all(np.abs(got[b, g, :n[b]] - want) <= _sums_bound(qq, kk, scale, window, want, D)), (b, g)
+
+
 def test_refusals(fs):
     """Nothing is launched: the counter of launches stays."""
     from rank_transformer_b200.kv8 import KV8Cache
