@@ -40,6 +40,10 @@
 // launch twice as long, 33 us.)  2048 tokens of one sequence (32 heads) take
 // 13 us for 2.6 us of bytes: launch, first loads, the join of the warps and
 // of the CTAs follow one another.
+// CTAs with equal work do not end together (long rows: after 77 to 100 us, 87
+// on average): memory serves some SMs better.  Handing out the work as they
+// come would even that out, but either the order of the sums would change from
+// call to call or every few blocks would leave a partial of 4 KB.
 #include "kv8.cuh"
 #include "tc.cuh"
 
