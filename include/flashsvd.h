@@ -380,9 +380,12 @@ FLASHSVD_API int flashsvd_kv8_store(const flashsvd_bf16* k_rows, const flashsvd_
  * head: added to it when accumulate != 0 (the entry of a token appended by
  * this call is set, not added to), written when accumulate is 0.  Entries
  * beyond cache_seqlens[b] are left alone.
- * At most 16 query heads per KV head, B <= 1024.  With weights, H * S_max
- * floats of the context's workspace (64 MiB) hold one batch row's scores: a
- * call with a larger row returns FLASHSVD_ERR_UNSUPPORTED_SHAPE. */
+ * At most 16 query heads per KV head, B <= 1024.  With weights the scores
+ * (S_max floats a query head, whatever the rows hold) go through 2^24 floats
+ * of the context's workspace: where those of all B rows do not fit, the call
+ * runs as several pairs of launches, over some of the batch rows or of one
+ * row's KV heads at a time (about 19 us a pair); where those of one KV head,
+ * (H / H_kv) * S_max, do not fit, it returns FLASHSVD_ERR_UNSUPPORTED_SHAPE. */
 FLASHSVD_API int flashsvd_kv8_decode_attn(const flashsvd_bf16* q, const flashsvd_bf16* k_new,
                                           const flashsvd_bf16* v_new, const flashsvd_kv8* cache,
                                           const int32_t* cache_seqlens, float* weights, int accumulate,

@@ -817,31 +817,39 @@ int kv8_attn_launch(const Kv8AttnParams& a, int sm_count, cudaStream_t stream) {
   const long long part = 2LL * workers * slot;
   if (part + 2LL * a.c.B * a.H > a.part_cap || (long long)a.c.B * a.c.G > a.counters_cap)
     return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
-  // With weights: the scores of as many batch rows as the workspace holds
-  // per pair of launches, the rows spread evenly over the pairs.
-  int step = a.c.B;
+  // With weights: the scores of as many batch rows as the workspace holds per
+  // pair of launches, the rows spread evenly over the pairs; where one row's
+  // do not fit, its KV heads are cut in the same way.
+  int step = a.c.B, heads = a.c.G;
   if (a.weights) {
-    const long long fit = a.scores_cap / ((long long)a.H * a.c.S_max);
+    const long long fit = a.scores_cap / ((long long)rep * a.c.S_max);  // (batch row, KV head) pairs
     if (fit < 1) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
-    if (fit < step) step = ceil_div(a.c.B, ceil_div(a.c.B, (int)fit));
+    if (fit < a.c.G) {
+      step = 1;
+      heads = ceil_div(a.c.G, ceil_div(a.c.G, (int)fit));
+    } else if (fit / a.c.G < step) {
+      step = ceil_div(a.c.B, ceil_div(a.c.B, (int)(fit / a.c.G)));
+    }
   }
-  for (int b0 = 0; b0 < a.c.B; b0 += step) {
-    const int nb = a.c.B - b0 < step ? a.c.B - b0 : step;
+  const int cuts = ceil_div(a.c.G, heads);
+  for (int i = 0; i < ceil_div(a.c.B, step) * cuts; ++i) {
+    const int b0 = i / cuts * step, g0 = i % cuts * heads;
+    const int nb = a.c.B - b0 < step ? a.c.B - b0 : step, ng = a.c.G - g0 < heads ? a.c.G - g0 : heads;
     KaParams p;
     p.c = a.c;
-    p.c.B = nb;
-    const long long pr = (long long)b0 * a.c.G;
+    p.c.B = nb; p.c.G = ng;  // (fewer heads than G: one row, whose heads are contiguous)
+    const long long pr = (long long)b0 * a.c.G + g0;
     for (int x = 0; x < 2; ++x) {
       p.c.codes[x] += pr * a.c.S_max * a.c.D;
       p.c.scale[x] += pr * (a.c.S_max / KV8_BLOCK);
       p.c.tail[x] += pr * KV8_BLOCK * a.c.D;
     }
-    p.q = a.q + (long long)b0 * a.H * a.c.D;
+    p.q = a.q + pr * rep * a.c.D;
     p.k_new = a.k_new ? a.k_new + pr * a.c.D : nullptr;
     p.v_new = a.v_new ? a.v_new + pr * a.c.D : nullptr;
-    p.out = a.out + (long long)b0 * a.H * a.c.D;
+    p.out = a.out + pr * rep * a.c.D;
     p.seqlens = a.seqlens + b0;
-    p.H = a.H; p.rep = rep;
+    p.H = ng * rep; p.rep = rep;
     p.scale_log2 = a.scale_log2;
     p.part = a.part;
     p.counters = a.counters;
@@ -849,7 +857,7 @@ int kv8_attn_launch(const Kv8AttnParams& a, int sm_count, cudaStream_t stream) {
     p.ml = a.part + part;
     p.scores = a.scores;
     // the cache length is only known on the device: the tag counts the capacity
-    const double kv = 2.0 * nb * a.c.G * (double)a.c.S_max * a.c.D;
+    const double kv = 2.0 * nb * ng * (double)a.c.S_max * a.c.D;
     const LaunchTag tag{"kv8_decode_attn", kv, 2.0 * kv * rep};
     int st;
     if (a.c.D == 128)
@@ -863,10 +871,10 @@ int kv8_attn_launch(const Kv8AttnParams& a, int sm_count, cudaStream_t stream) {
       KwParams w;
       w.scores = p.scores; w.ml = p.ml; w.seqlens = p.seqlens;
       w.weights = a.weights + pr * a.c.S_max;
-      w.G = a.c.G; w.H = a.H; w.rep = rep; w.S_max = a.c.S_max;
+      w.G = ng; w.H = p.H; w.rep = rep; w.S_max = a.c.S_max;
       w.accumulate = a.accumulate; w.fresh = a.k_new != nullptr;
-      const LaunchTag wt{"kv8_weights", 4.0 * nb * (a.H + 2.0 * a.c.G) * a.c.S_max, 0.0};
-      const int pairs = nb * a.c.G;
+      const LaunchTag wt{"kv8_weights", 4.0 * nb * (p.H + 2.0 * ng) * a.c.S_max, 0.0};
+      const int pairs = nb * ng;
       if (pairs > 65535) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
       FSVD_TRY(launch_pdl(wt, kv8_weights_kernel, dim3(ceil_div(a.c.S_max, KW_THREADS * 4), pairs), dim3(KW_THREADS), 0,
                           stream, w));

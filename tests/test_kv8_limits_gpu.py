@@ -1,0 +1,85 @@
+"""The 8-bit cache operators at the ends of their ranges: capacities whose
+scores do not fit the workspace at once, against the float64 oracle."""
+import numpy as np
+import pytest
+
+from oracle import flashsvd_oracle as oracle
+from tests.test_kv8_gpu import U32, _attend_bound, _bf16, _dev, _rows
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def fs():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from rank_transformer_b200 import flashsvd
+    flashsvd.init(0, max_tokens=512, max_rank=512, max_hidden=1024, max_ffn=2048)
+    return flashsvd
+
+
+class _Step:
+    """A decode step over rows of n[b] tokens and its comparison with the
+    oracle: outputs and, unless None, the weights w added to w0."""
+
+    def __init__(self, fs, fmt, n, G, rep, D, S_max, seed, scale=0.125, vstd=1.0):
+        from rank_transformer_b200.kv8 import KV8Cache
+        rng = np.random.default_rng(seed)
+        B, S = len(n), max(n) + 1
+        self.fs, self.n, self.G, self.rep, self.D, self.S_max, self.fmt, self.scale = fs, n, G, rep, D, S_max, fmt, scale
+        self.k, self.v = _rows(rng, (B, S, G, D), False), _bf16(vstd * _rows(rng, (B, S, G, D)))
+        self.q = _bf16(1.5 * rng.standard_normal((B, G * rep, D)))
+        self.cache = KV8Cache(B, G, D, S_max, fmt)
+        self.dn = _dev(n, torch.int32)
+        fs.kv8_store(_dev(self.k), _dev(self.v), self.cache, self.dn, S, S)
+        self.kn = np.stack([self.k[b, n[b]] for b in range(B)])
+        self.vn = np.stack([self.v[b, n[b]] for b in range(B)])
+
+    def run(self, w):
+        out = torch.full((len(self.n), self.G * self.rep, self.D), 7.0, dtype=torch.bfloat16, device="cuda")
+        self.fs.kv8_decode_attn(_dev(self.q), _dev(self.kn), _dev(self.vn), self.cache, self.dn, w, True, out,
+                                self.G * self.rep, self.scale)
+        torch.cuda.synchronize()
+        self.fs.check_device_status()
+        return out
+
+    def check(self, out, w, w0):
+        got, rep = out.double().cpu().numpy(), self.rep
+        for b, n in enumerate(self.n):
+            for g in range(self.G):
+                kx = oracle.kv8_rows(self.k[b, :n + 1, g], self.fmt)
+                vx = oracle.kv8_rows(self.v[b, :n + 1, g], self.fmt)
+                add, worst = np.zeros(n + 1), 0.0
+                for h in range(g * rep, (g + 1) * rep):
+                    p = oracle.attention_probs(self.q[b, h][None], kx, self.scale)[0]
+                    want = p @ vx
+                    e_out, eps_p = _attend_bound(self.q[b, h], kx, vx, p, self.scale, want)
+                    err = np.abs(got[b, h] - want)
+                    assert np.all(err <= e_out), (b, h, float(np.max(err / e_out)))
+                    add += p
+                    worst = max(worst, eps_p)
+                if w is None:
+                    continue
+                base = np.full(n + 1, w0)
+                base[n] = 0.0     # the appended token's entry is set
+                wg = w[b, g, :n + 1].double().cpu().numpy()
+                assert np.all(np.abs(wg - base - add) <= worst * add + 4 * U32 * (base + add) + 2.0 ** -100), (b, g)
+                assert (w[b, g, n + 1:] == w0).all()
+
+
+@pytest.mark.parametrize("fmt,n,G,rep,D,S_max,launches", [
+    ("int8", [300, 64], 20, 2, 64, 524288, 2 * 2 * 2),    # 16 KV heads' scores fit: 10 and 10 a row
+    ("e4m3", [127], 3, 16, 128, 400000, 2 * 2),           # 2 fit: 2 and 1
+    ("int8", [70, 0, 5], 2, 8, 64, 1048576, 3 * 2),       # 2 fit: both heads of a row
+])
+def test_scores_of_a_row_cut_by_heads(fs, fmt, n, G, rep, D, S_max, launches):
+    """With weights, the scores of one batch row may pass the workspace: the
+    call runs over some of its KV heads at a time."""
+    s = _Step(fs, fmt, n, G, rep, D, S_max, 31)
+    w = torch.full((len(n), G, S_max), 2.0, device="cuda")
+    before = fs.lib.flashsvd_launch_count()
+    out = s.run(w)
+    assert fs.lib.flashsvd_launch_count() - before == launches
+    s.check(out, w, 2.0)
