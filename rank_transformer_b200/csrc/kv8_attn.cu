@@ -27,6 +27,15 @@
 // scaling by 2^15, so that they keep 11 bits down to 2^-29 and vanish only
 // below 2^-40 of the largest; l is summed from the unrounded ones.
 //
+// Range.  O / l is at most the largest |v|, but O alone is up to n times as
+// large.  The output sums carry 2^-K, 2^(K - 1) >= S_max (one more bit than n
+// needs: rounding may take a probability a little over 1), through the value
+// scales, and its inverse at the end: values up to the last bf16 number do not
+// overflow.  Each addition may then be off by 2^(K - 149), which is below half
+// a step of a bf16 output unless that is itself near 2^-126.  (K by capacity,
+// a launch's constant: one by the pair's length took a register and with it
+// 246 us where this takes 242, 4 rows of 131071 tokens with weights.)
+//
 // Bound by HBM where histories are long: 32 rows of up to 8191 tokens, 8 KV
 // heads of 128, take 55-58 us (46 for the bytes), 4 rows of 131071 tokens
 // without weights 164 us (163).  What it took there: rings of TMA loads in
@@ -44,6 +53,8 @@
 // on average): memory serves some SMs better.  Handing out the work as they
 // come would even that out, but either the order of the sums would change from
 // call to call or every few blocks would leave a partial of 4 KB.
+#include <cmath>
+
 #include "kv8.cuh"
 #include "tc.cuh"
 
@@ -61,7 +72,7 @@ constexpr int KA_PAIR_COST = 12;
 // 4 and 8 units 8.4, 8.8, 9.4, 10.9 / 10.4, 10.5, 11.5, 12.2 us; with 2 the two
 // blocks of a 100-token history still stay together).
 constexpr int KA_MIN_UNITS = 2;
-constexpr float KA_PSHIFT = 15.f;  // probabilities carry a factor 2^15 (it cancels in O / l)
+constexpr int KA_PSHIFT = 15;  // probabilities and l carry a factor 2^15
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -97,6 +108,7 @@ struct KaParams {
   bf16* out;
   int H, rep;                  // query heads, query heads per KV head
   float scale_log2;
+  float vdown, vup;            // 2^-(K + 15) on the values (15: KA_PSHIFT), its inverse on O / l
   float* part;                 // [2 * workers][KaLayout::SLOT] partials
   int* counters;               // [B * G] contributors done, zero between launches
   float* scores; float* ml;    // weights wanted: x_j [B * H][S_max]; (M, 1 / l) [B * H][2]
@@ -397,7 +409,10 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         softmax_step<MT, NT>(x[nt], m[nt], l[nt], acc, nt);
         float r4[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) r4[r] = x[nt][r] - bf2f(f2bf(x[nt][r]));
+        for (int r = 0; r < 4; ++r) {
+          x[nt][r] *= p.vdown;
+          r4[r] = x[nt][r] - bf2f(f2bf(x[nt][r]));
+        }
         ph[nt][0] = transpose8x8(pack_bf2(x[nt][0], x[nt][1]));
         ph[nt][1] = transpose8x8(pack_bf2(x[nt][2], x[nt][3]));
         pl[nt][0] = transpose8x8(pack_bf2(r4[0], r4[1]));
@@ -437,7 +452,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
       const int st = uses % NST;
       const uint8_t* kh = ring + st * 2 * L::HALF;
       const uint8_t* vh = kh + L::HALF;
-      sk = sk_next; sv = sv_next;
+      sk = sk_next; sv = sv_next * p.vdown;
       if (s + KA_WARPS < n_code) { sk_next = ks[(s + KA_WARPS) >> 2]; sv_next = vs[(s + KA_WARPS) >> 2]; }
       if (!tc::mbar_wait(bar + st, (uint32_t)(uses / NST) & 1u, &s_abort, p.status)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
@@ -573,7 +588,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
       }
       if (whole) {
-        const float r = 1.f / s_l[h];
+        const float r = p.vup / s_l[h];
         *reinterpret_cast<uint2*>(p.out + (long long)h0 * D + i) =
             make_uint2(pack_bf2(o.x * r, o.y * r), pack_bf2(o.z * r, o.w * r));
       } else {
@@ -707,7 +722,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (groups > 1) {
           *reinterpret_cast<float4*>(red + 4 * (grp * nv + i)) = o;
         } else {
-          const float r = 1.f / s_l[h];
+          const float r = p.vup / s_l[h];
           *reinterpret_cast<uint2*>(p.out + (long long)h0 * D + 4 * i) =
               make_uint2(pack_bf2(o.x * r, o.y * r), pack_bf2(o.z * r, o.w * r));
         }
@@ -721,7 +736,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
           const float4 w = *reinterpret_cast<const float4*>(red + 4 * (k * nv + tid));
           o.x += w.x; o.y += w.y; o.z += w.z; o.w += w.w;
         }
-        const float r = 1.f / s_l[4 * tid / D];
+        const float r = p.vup / s_l[4 * tid / D];
         *reinterpret_cast<uint2*>(p.out + (long long)h0 * D + 4 * tid) =
             make_uint2(pack_bf2(o.x * r, o.y * r), pack_bf2(o.z * r, o.w * r));
       }
@@ -831,6 +846,8 @@ int kv8_attn_launch(const Kv8AttnParams& a, int sm_count, cudaStream_t stream) {
       step = ceil_div(a.c.B, ceil_div(a.c.B, (int)(fit / a.c.G)));
     }
   }
+  int K = 1;
+  while ((1LL << (K - 1)) < a.c.S_max) ++K;
   const int cuts = ceil_div(a.c.G, heads);
   for (int i = 0; i < ceil_div(a.c.B, step) * cuts; ++i) {
     const int b0 = i / cuts * step, g0 = i % cuts * heads;
@@ -851,6 +868,8 @@ int kv8_attn_launch(const Kv8AttnParams& a, int sm_count, cudaStream_t stream) {
     p.seqlens = a.seqlens + b0;
     p.H = ng * rep; p.rep = rep;
     p.scale_log2 = a.scale_log2;
+    p.vup = std::ldexp(1.f, KA_PSHIFT + K);
+    p.vdown = 1.f / p.vup;
     p.part = a.part;
     p.counters = a.counters;
     p.status = a.status;

@@ -1,5 +1,8 @@
 """The 8-bit cache operators at the ends of their ranges: capacities whose
-scores do not fit the workspace at once, against the float64 oracle."""
+scores do not fit the workspace at once, values near the ends of bf16's range;
+against the float64 oracle."""
+import math
+
 import numpy as np
 import pytest
 
@@ -56,6 +59,14 @@ class _Step:
                     p = oracle.attention_probs(self.q[b, h][None], kx, self.scale)[0]
                     want = p @ vx
                     e_out, eps_p = _attend_bound(self.q[b, h], kx, vx, p, self.scale, want)
+                    # Below 2^-126 steps are absolute.  Output: bf16's are 2^-133,
+                    # half of one 2^-134.  Sums: they carry 2^-shift, 2^(shift - 1)
+                    # the least power of two from S_max on, and each of n + 1
+                    # additions is off by at most fp32's least step, 2^-149 (matrix
+                    # instructions cut off); divided by a sum of probabilities of
+                    # 1 or more, that is 2^(shift - 149) each.
+                    shift = math.ceil(math.log2(self.S_max)) + 1
+                    e_out = e_out + 2.0 ** -134 + (n + 1) * 2.0 ** (shift - 149)
                     err = np.abs(got[b, h] - want)
                     assert np.all(err <= e_out), (b, h, float(np.max(err / e_out)))
                     add += p
@@ -83,3 +94,24 @@ def test_scores_of_a_row_cut_by_heads(fs, fmt, n, G, rep, D, S_max, launches):
     out = s.run(w)
     assert fs.lib.flashsvd_launch_count() - before == launches
     s.check(out, w, 2.0)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("power", [118, -108])
+@pytest.mark.parametrize("n,G,rep,D,S_max", [
+    ([4090, 5], 1, 2, 64, 4096),
+    ([2047, 64, 0], 2, 1, 128, 2048),
+    ([1500], 1, 12, 128, 1536),
+    ([63, 190, 128], 3, 9, 64, 192),
+])
+def test_values_at_the_ends_of_the_range(fmt, power, fs, n, G, rep, D, S_max):
+    """Output sums are up to n times the output: values of up to 2^126.5 (and
+    down to where the scale of a block is at its floor) give what the
+    definition gives, with attention spread over all tokens (scale 2^-6) and
+    on a few."""
+    for scale in (2.0 ** -6, 0.25):
+        s = _Step(fs, fmt, n, G, rep, D, S_max, 41 + D, scale=scale, vstd=2.0 ** power)
+        assert np.isfinite(s.v).all() and np.abs(s.v).max() > 2.0 ** (power + 6)
+        out = s.run(None)
+        assert torch.isfinite(out).all()
+        s.check(out, None, 0.0)
