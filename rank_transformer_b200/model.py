@@ -211,13 +211,12 @@ class DecoderModel:
         cfg = self.cfg
         x = torch.empty((B * S, cfg.d), dtype=torch.bfloat16, device=self.device)
         fs.embed(prompt.reshape(-1), self.emb, x, B * S, cfg.d, cfg.vocab, stream)
-        if self.kv_format is not None and (self.kv_rows is None or self.kv_rows.shape[1] != B * S):
-            if self.kv_rows is not None and stream is not None:
-                self.kv_rows.record_stream(stream)  # an earlier prompt's work may still use it
-            self.kv_rows = torch.empty((2, B * S, cfg.d), dtype=torch.bfloat16, device=self.device)
+        if self.kv_format is not None:
+            with torch.cuda.stream(stream):
+                rows = self._prompt_rows(B * S)
         for i in range(cfg.layers):
             if self.kv_format is not None:
-                fs.layer_forward_kv8(self.structs[i], x, self.kv8[i], self.kv_rows[0], self.kv_rows[1],
+                fs.layer_forward_kv8(self.structs[i], x, self.kv8[i], rows[0], rows[1],
                                      self.kv_weights[i], self.kv_window, None, None, self.max_positions, B, S,
                                      fs.PREFILL_CAUSAL, stream)
                 continue
@@ -236,6 +235,16 @@ class DecoderModel:
             self.positions.fill_(S)
         self.length = self.position = S
         return x
+
+    def _prompt_rows(self, n: int):
+        """Scratch [2, n, d] for n tokens' key and value rows on torch's
+        current stream, kept from prompt to prompt.  The allocator is told of
+        every stream that uses it, so that one which is replaced is not handed
+        out while an earlier prompt's work may still use it."""
+        if self.kv_rows is None or self.kv_rows.shape[1] != n:
+            self.kv_rows = torch.empty((2, n, self.cfg.d), dtype=torch.bfloat16, device=self.device)
+        self.kv_rows.record_stream(torch.cuda.current_stream(self.kv_rows.device))
+        return self.kv_rows
 
     # ----------------------------------------------------------- decode --
     def _head(self, stream):
