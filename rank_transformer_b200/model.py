@@ -207,13 +207,15 @@ class DecoderModel:
         """prompt: device int32 [B, S].  Runs every layer over the whole
         prompt (writing cache rows [0, S)), then the head on the last
         position; sets cache_seqlens = S and the next tokens."""
+        with torch.cuda.stream(stream):  # (torch's own kernels and buffers too)
+            return self._prefill(prompt, stream)
+
+    def _prefill(self, prompt, stream):
         B, S = prompt.shape
         cfg = self.cfg
         x = torch.empty((B * S, cfg.d), dtype=torch.bfloat16, device=self.device)
         fs.embed(prompt.reshape(-1), self.emb, x, B * S, cfg.d, cfg.vocab, stream)
-        if self.kv_format is not None:
-            with torch.cuda.stream(stream):
-                rows = self._prompt_rows(B * S)
+        rows = self._prompt_rows(B * S) if self.kv_format is not None else None
         for i in range(cfg.layers):
             if self.kv_format is not None:
                 fs.layer_forward_kv8(self.structs[i], x, self.kv8[i], rows[0], rows[1],
@@ -392,6 +394,10 @@ class DecoderModel:
         -> host int32 tokens [B, steps].  Copies the prompt in, prefills,
         decodes ``steps`` greedy tokens with the captured graphs and copies
         the generated tokens out."""
+        with torch.cuda.stream(stream):  # (the copies too)
+            return self._generate(prompt_host, steps, stream)
+
+    def _generate(self, prompt_host, steps, stream):
         B, S = prompt_host.shape
         prompt = prompt_host.to(self.device, non_blocking=True)
         gen = torch.empty((steps, B), dtype=torch.int32, device=self.device)

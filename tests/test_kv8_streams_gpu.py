@@ -44,3 +44,36 @@ def test_replaced_prompt_scratch_is_not_handed_out(fs):
         assert not side.query(), "the stream was to be busy"
         assert at not in [t.data_ptr() for t in free]
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["int8", None])
+def test_everything_runs_on_the_given_stream(fs, fmt):
+    """prefill on a side stream leaves nothing behind the work that the current
+    stream still has to do; generate gives the same tokens there."""
+    prompt = torch.randint(0, 1000, (2, 100), dtype=torch.int32, generator=torch.Generator().manual_seed(4)).pin_memory()
+    m = _model(fmt)
+    side = torch.cuda.Stream()
+    m.capture(side)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        want = m.generate(prompt, 9, side)
+    side.synchronize()
+    lengths = [m.seqlens] + ([m.positions] if fmt else [])
+    on_device = prompt.cuda()
+    torch.cuda.synchronize()
+    for busy in (False, True):  # (once before: first launches and allocations wait for the device)
+        m.seqlens.zero_()
+        torch.cuda.synchronize()
+        if busy:
+            torch.cuda._sleep(BUSY)
+        m.prefill(on_device, side)
+        with torch.cuda.stream(side):
+            got = torch.stack(lengths).cpu()   # waits for `side` alone
+        assert (got == 100).all()
+    assert not torch.cuda.current_stream().query(), "the stream was to be busy"
+    tokens = m.generate(prompt, 9, side)
+    side.synchronize()
+    assert torch.equal(tokens, want)
+    torch.cuda.synchronize()
+    fs.check_device_status()
+    m.release_graphs()
