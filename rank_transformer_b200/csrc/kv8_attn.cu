@@ -63,7 +63,6 @@ namespace {
 
 constexpr int KA_WARPS = 8;
 constexpr int KA_THREADS = 32 * KA_WARPS;
-constexpr int KA_MAX_WORKERS = 512;  // partials of one pair that the joining CTA has room for
 // What a pair costs beside its blocks, in blocks (work split): joins, the
 // append and the first loads.  (64 rows of up to 600 tokens x 8 heads: 40 us
 // with 0, 23.7 with 12; 32 rows of up to 8191: 58 and 52.)
@@ -125,6 +124,10 @@ struct KaLayout {
   static constexpr int NST = (NT == 1 ? 2 : 4) * (128 / D);  // ring stages of a warp
   static constexpr int RING = KA_WARPS * NST * 2 * HALF;
   static constexpr int O_OFF = RING;              // [warps][HP][OP] floats
+  // Workers whose partials of one pair the joining CTA has room for: a factor
+  // per head each, beside four sums a thread, where the warps' O were.
+  static constexpr int JOIN = (KA_WARPS * HP * OP - 4 * KA_THREADS) / HP;
+  static_assert(148 * CTAS <= JOIN, "the CTAs of a B200");
   static constexpr int ML_OFF = O_OFF + KA_WARPS * HP * OP * 4;    // m, l, factor: [3][warps][HP] floats
   static constexpr int BAR_OFF = ML_OFF + 3 * KA_WARPS * HP * 4;
   static constexpr int SMEM = 1024 + BAR_OFF + KA_WARPS * NST * 8;
@@ -661,7 +664,7 @@ kv8_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const int late = first_of(w0) < pair0 ? 1 : 0;  // the pair is the last one of its first worker
     auto slot_of = [&](int k) { return p.part + (long long)(2 * (w0 + k) + (k == 0 ? late : 0)) * L::SLOT; };
     float* fac = s_o;                         // [nc][HP] factors
-    float* red = s_o + ((nc * HP + 3) & ~3);  // [groups][rep * D] sums
+    float* red = s_o + nc * HP;               // [groups][rep * D] sums
     // vectors of four sums; with few of them, groups of threads share the
     // partials.  A batch of loads is in flight while the factors are formed.
     constexpr int BATCH = 16;
@@ -799,6 +802,7 @@ kv8_weights_kernel(const __grid_constant__ KwParams p) {
 template <int D, int NT>
 int launch_ka(const KaParams& p, bool scores, int workers, const LaunchTag& tag, cudaStream_t s) {
   using L = KaLayout<D, NT>;
+  if (workers > L::JOIN) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
   CUtensorMap mk, mv;
   const long long rows = (long long)p.c.B * p.c.G * p.c.S_max * D / 128;
   if (rows > 0x7fffffffLL) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
@@ -826,7 +830,7 @@ int kv8_attn_launch(const Kv8AttnParams& a, int sm_count, cudaStream_t stream) {
   const int rep = a.H / a.c.G, NT = rep <= 8 ? 1 : 2;
   if (rep > 16 || a.c.B > KV8_MAX_BATCH) return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
   const int workers = sm_count * (NT == 1 ? 2 : 1);
-  if (workers > KA_MAX_WORKERS || (long long)a.c.B * a.c.G * (a.c.S_max / KV8_BLOCK + KA_PAIR_COST) > 0x3fffffffLL)
+  if ((long long)a.c.B * a.c.G * (a.c.S_max / KV8_BLOCK + KA_PAIR_COST) > 0x3fffffffLL)
     return FLASHSVD_ERR_UNSUPPORTED_SHAPE;
   const long long slot = 2 * 8 * NT + 8LL * NT * a.c.D;
   const long long part = 2LL * workers * slot;
