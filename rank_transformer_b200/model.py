@@ -278,6 +278,9 @@ class DecoderModel:
                              self.seqlens, self.B, 1, self.S_max, fs.DECODE, stream)
 
     def decode_step_eager(self, stream=None):
+        """One decode step without graphs.  (Like decode_step, an 8-bit model
+        whose cache is full raises ValueError: evict first.)"""
+        self._check_room()
         cfg = self.cfg
         fs.embed(self.tokens, self.emb, self.x, self.B, cfg.d, cfg.vocab, stream)
         self._layers_decode(stream)
@@ -302,6 +305,13 @@ class DecoderModel:
         """Before a decode step of ``generate``: evict if the cache is full."""
         if self.kv_keep is not None and self.length >= self.S_max:
             self.evict(stream)
+        self._check_room()
+
+    def _check_room(self):
+        """Refuse a step of an 8-bit model for which there is no row or no
+        position: it would overwrite the newest token."""
+        if self.kv_format is None:
+            return
         if self.length >= self.S_max or self.position >= self.max_positions:
             raise ValueError(f"no room for another token: {self.length} of {self.S_max} cached, "
                              f"position {self.position} of {self.max_positions}")
@@ -336,6 +346,7 @@ class DecoderModel:
         self.step_graph = fs.graph_compose(self.graphs) if compose else None
 
     def decode_step(self, stream=None):
+        self._check_room()
         if self.step_graph is not None:
             self.step_graph.replay(stream)
         else:

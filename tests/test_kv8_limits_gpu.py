@@ -115,3 +115,25 @@ def test_values_at_the_ends_of_the_range(fmt, power, fs, n, G, rep, D, S_max):
         out = s.run(None)
         assert torch.isfinite(out).all()
         s.check(out, None, 0.0)
+
+
+def test_a_full_model_refuses_a_step(fs):
+    """At capacity a step raises and leaves everything as it was; after an
+    eviction it runs."""
+    from rank_transformer_b200.model import DecoderConfig, DecoderModel
+    cfg = DecoderConfig(layers=2, d=256, H=4, D=64, f=704, vocab=1000, rho=(0.5,))
+    m = DecoderModel(cfg, B=2, S_max=128, seed=3, kv_format="int8", kv_keep=70, max_positions=300)
+    m.prefill(torch.randint(0, 1000, (2, 127), dtype=torch.int32, device="cuda"))
+    m.decode_step_eager()
+    torch.cuda.synchronize()
+    state = lambda: [t.clone() for c in m.kv8 for t in c.tensors()] + [m.seqlens.clone(), m.kv_weights[1].clone()]  # noqa: E731
+    before = state()
+    with pytest.raises(ValueError, match="no room"):
+        m.decode_step_eager()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, state()))
+    m.evict()
+    m.decode_step_eager()
+    torch.cuda.synchronize()
+    fs.check_device_status()
+    assert m.length == 71 and m.seqlens.tolist() == [71, 71] and m.positions.tolist() == [129, 129]
