@@ -366,15 +366,29 @@ class DecoderModel:
         self.graphs, self.step_graph = None, None
 
     # ---------------------------------------------------------- bytes ---
+    def _kv_step_bytes(self, context: int) -> int:
+        """Bytes of the caches that one decode step cannot do without, all
+        layers: the history once and the new rows.  An 8-bit cache: the codes
+        and scales of the full blocks, the bf16 tail's rows and, with kv_keep,
+        every token's weight read and written (the scores that pass through
+        the workspace for it are not counted)."""
+        cfg = self.cfg
+        if self.kv_format is None:
+            return 2 * cfg.layers * (context + 1) * cfg.d * 2 * self.B
+        full = context // fs.KV8_BLOCK * fs.KV8_BLOCK
+        row = 2 * full * cfg.d + 2 * 4 * cfg.H * (full // fs.KV8_BLOCK) + 2 * 2 * (context - full + 1) * cfg.d
+        if self.kv_keep is not None:
+            row += 4 * cfg.H * (2 * context + 1)
+        return cfg.layers * self.B * row
+
     def decode_step_bytes(self, context: int) -> int:
         """Algorithmic HBM bytes of one decode step at cache length
         ``context`` (before the step): every factor and the LM head once,
         the K/V history of every layer once, the new K/V rows, and the
         activations in and out (negligible)."""
         cfg = self.cfg
-        kv = 2 * cfg.layers * (context + 1) * cfg.d * (1 if self.kv_format else 2) * self.B
         act = self.B * cfg.d * 2 * 2 * cfg.layers
-        return self.weight_bytes() + kv + act
+        return self.weight_bytes() + self._kv_step_bytes(context) + act
 
     def layers_decode_bytes(self, context: int) -> int:
         """Algorithmic HBM bytes of the decoder layers of one decode step
@@ -382,10 +396,8 @@ class DecoderModel:
         gains once, its K/V history at cache length ``context`` plus the new
         rows, and the activations in and out."""
         cfg = self.cfg
-        n = self._unique_params()
-        kv = 2 * cfg.layers * (context + 1) * cfg.d * 2 * self.B
         act = self.B * cfg.d * 2 * 2 * cfg.layers
-        return 2 * n + kv + act
+        return 2 * self._unique_params() + self._kv_step_bytes(context) + act
 
     def prefill_flops(self, S: int) -> float:
         """Algorithmic FLOPs of one prefill of B prompts of S tokens: every
