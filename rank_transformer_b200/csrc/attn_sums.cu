@@ -35,11 +35,12 @@
 // exponentials on the FMA pipe (201 us at 4096 tokens), 256 stationary rows
 // (207: half the traffic from L2), 128 x 128 tiles in two CTAs with one S
 // buffer (190), the same with the next item's operand in tensor memory ahead
-// of time (191), and with the next tile's scores loaded ahead too (203).  Without the exponentials 4096 tokens take 159 us, without
-// seven eighths of the products 187, without both 120: the chain of waits,
-// tensor-memory loads and hand-offs of a tile (900 clocks), the exponentials
-// and the products each fill most of the time, and four warps per scheduler,
-// all that registers allow, overlap them to 0.65 of the exponentials' rate.
+// of time (191), and with the next tile's scores loaded ahead too (203).
+// Without the exponentials 4096 tokens take 159 us, without seven eighths of
+// the products 187, without both 120: the chain of waits, tensor-memory loads
+// and hand-offs of a tile (900 clocks), the exponentials and the products each
+// fill most of the time, and four warps per scheduler, all that registers
+// allow, overlap them to 0.65 of the exponentials' rate.
 // Every wait is bounded.
 #include <cstring>
 
@@ -381,98 +382,98 @@ attn_stats_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     int i = 0, j = 0, t = 0, done = 0;  // items: of the list, with products, finished
     SuItem next = su_item(p, min(su_index(0), items - 1), true);
     for (; su_index(i) < items; ++i) {
-    const SuItem it = next;
-    if (su_index(i + 1) < items) next = su_item(p, su_index(i + 1), true);  // (its length arrives meanwhile)
-    const SuRow R(p, it.len);
-    const SuStats w(p, it, R);
-    if (!w.live(p, it, R)) continue;
-    const int half = row >> 6;
-    const int run = half ? w.run[1] : w.run[0], head = half ? w.head[1] : w.head[0];
-    const bool mine = half == 0 || w.two;
-    const int q = R.lo + run * SU_RUN + (row & 63);  // query position
-    float* lse = p.lse + ((long long)(it.b * p.H + it.g * p.rep + head) * p.runs + run) * SU_RUN + (row & 63);
-    float m = -INFINITY, l = 0.f;
-    if (grp == 0 && w.n > 0) ok = su_a_to_tmem<D>(bars, smem, tmem, j, row, lane, p.status) && ok;
-    for (int k = t + grp; k < t + w.n; k += 2) {
-      const int sb = k % L::NS, key0 = (w.t0 + k - t) * SU_RUN;
-      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->s_full + sb, (uint32_t)(k / L::NS) & 1u, &bars->abort_flag,
-                                                       p.status));
-      // (two bodies, with the load in them: with one load and a branch around
-      // the mask alone every tile paid for the mask's selects)
-      auto tile = [&](auto diagonal) {
-        float s[64];
-        su_scores(s, tmem + lane_base + L::TM_S + sb * SU_RUN);
-        if (lane == 0) tc::mbar_arrive(bars->s_empty + sb);
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          if (diagonal.value) {
-            s[c] = key0 + c > q ? -INFINITY : s[c];
-            s[c + 1] = key0 + c + 1 > q ? -INFINITY : s[c + 1];
+      const SuItem it = next;
+      if (su_index(i + 1) < items) next = su_item(p, su_index(i + 1), true);  // (its length arrives meanwhile)
+      const SuRow R(p, it.len);
+      const SuStats w(p, it, R);
+      if (!w.live(p, it, R)) continue;
+      const int half = row >> 6;
+      const int run = half ? w.run[1] : w.run[0], head = half ? w.head[1] : w.head[0];
+      const bool mine = half == 0 || w.two;
+      const int q = R.lo + run * SU_RUN + (row & 63);  // query position
+      float* lse = p.lse + ((long long)(it.b * p.H + it.g * p.rep + head) * p.runs + run) * SU_RUN + (row & 63);
+      float m = -INFINITY, l = 0.f;
+      if (grp == 0 && w.n > 0) ok = su_a_to_tmem<D>(bars, smem, tmem, j, row, lane, p.status) && ok;
+      for (int k = t + grp; k < t + w.n; k += 2) {
+        const int sb = k % L::NS, key0 = (w.t0 + k - t) * SU_RUN;
+        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->s_full + sb, (uint32_t)(k / L::NS) & 1u, &bars->abort_flag,
+                                                         p.status));
+        // (two bodies, with the load in them: with one load and a branch around
+        // the mask alone every tile paid for the mask's selects)
+        auto tile = [&](auto diagonal) {
+          float s[64];
+          su_scores(s, tmem + lane_base + L::TM_S + sb * SU_RUN);
+          if (lane == 0) tc::mbar_arrive(bars->s_empty + sb);
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  #pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            if (diagonal.value) {
+              s[c] = key0 + c > q ? -INFINITY : s[c];
+              s[c + 1] = key0 + c + 1 > q ? -INFINITY : s[c + 1];
+            }
+            m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], s[c], s[c + 1]);
           }
-          m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], s[c], s[c + 1]);
-        }
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
-        if (mx > m) {
-          l *= ex2f(m - mx);
-          m = mx;
-        }
-        const float e = m == -INFINITY ? 0.f : -m;
-        float a4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          fma2(s[c], s[c + 1], sc, e, e);
-          add2(a4[c & 2], a4[(c & 2) + 1], ex2f(s[c]), ex2f(s[c + 1]));
-        }
-        l += (a4[0] + a4[1]) + (a4[2] + a4[3]);
-      };
-      if (__any_sync(0xffffffffu, key0 + 63 > q))
-        tile(SuBool<true>{});
-      else
-        tile(SuBool<false>{});
-    }
-    t += w.n;
-    float2* x = xch + (done++ & 1) * 128 + row;  // (in turn: the last item's may still be read)
-    if (grp == 1) *x = make_float2(m, l);
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    const int cell = it.pair * p.row_tiles + it.t;  // row tile of the pair
-    if (grp == 0) {
-      const float2 o = *x;
-      const float M = fmaxf(m, o.x);
-      const float e = M == -INFINITY ? 0.f : M;
-      const float sum = l * ex2f(m - e) + o.y * ex2f(o.x - e);
-      if (p.splits == 1) {
-        if (mine) *lse = q < R.n ? -(M + log2f(sum)) : -INFINITY;
-      } else {
-        __stcg(p.part + ((long long)cell * p.splits + it.sp) * 128 + row, make_float2(M, sum));
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sc;
+          if (mx > m) {
+            l *= ex2f(m - mx);
+            m = mx;
+          }
+          const float e = m == -INFINITY ? 0.f : -m;
+          float a4[4] = {0.f, 0.f, 0.f, 0.f};
+  #pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            fma2(s[c], s[c + 1], sc, e, e);
+            add2(a4[c & 2], a4[(c & 2) + 1], ex2f(s[c]), ex2f(s[c + 1]));
+          }
+          l += (a4[0] + a4[1]) + (a4[2] + a4[3]);
+        };
+        if (__any_sync(0xffffffffu, key0 + 63 > q))
+          tile(SuBool<true>{});
+        else
+          tile(SuBool<false>{});
       }
-    }
-    if (p.splits > 1) {
-      __threadfence();
+      t += w.n;
+      float2* x = xch + (done++ & 1) * 128 + row;  // (in turn: the last item's may still be read)
+      if (grp == 1) *x = make_float2(m, l);
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (threadIdx.x == 64) {
-        const int old = atomicAdd(p.counters + cell, 1);
-        bars->last = old == p.splits - 1;
-        if (old == p.splits - 1) p.counters[cell] = 0;
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (bars->last && grp == 0 && mine) {
-        __threadfence();
-        const float2* src = p.part + (long long)cell * p.splits * 128 + row;
-        float M = -INFINITY;
-#pragma unroll 8
-        for (int z = 0; z < p.splits; ++z) M = fmaxf(M, __ldcg(src + z * 128).x);
+      const int cell = it.pair * p.row_tiles + it.t;  // row tile of the pair
+      if (grp == 0) {
+        const float2 o = *x;
+        const float M = fmaxf(m, o.x);
         const float e = M == -INFINITY ? 0.f : M;
-        float sum = 0.f;
-#pragma unroll 8
-        for (int z = 0; z < p.splits; ++z) {
-          const float2 o = __ldcg(src + z * 128);
-          sum += o.y * ex2f(o.x - e);
+        const float sum = l * ex2f(m - e) + o.y * ex2f(o.x - e);
+        if (p.splits == 1) {
+          if (mine) *lse = q < R.n ? -(M + log2f(sum)) : -INFINITY;
+        } else {
+          __stcg(p.part + ((long long)cell * p.splits + it.sp) * 128 + row, make_float2(M, sum));
         }
-        *lse = q < R.n ? -(M + log2f(sum)) : -INFINITY;
       }
-    }
-    if (w.n > 0) ++j;
+      if (p.splits > 1) {
+        __threadfence();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (threadIdx.x == 64) {
+          const int old = atomicAdd(p.counters + cell, 1);
+          bars->last = old == p.splits - 1;
+          if (old == p.splits - 1) p.counters[cell] = 0;
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (bars->last && grp == 0 && mine) {
+          __threadfence();
+          const float2* src = p.part + (long long)cell * p.splits * 128 + row;
+          float M = -INFINITY;
+  #pragma unroll 8
+          for (int z = 0; z < p.splits; ++z) M = fmaxf(M, __ldcg(src + z * 128).x);
+          const float e = M == -INFINITY ? 0.f : M;
+          float sum = 0.f;
+  #pragma unroll 8
+          for (int z = 0; z < p.splits; ++z) {
+            const float2 o = __ldcg(src + z * 128);
+            sum += o.y * ex2f(o.x - e);
+          }
+          *lse = q < R.n ? -(M + log2f(sum)) : -INFINITY;
+        }
+      }
+      if (w.n > 0) ++j;
     }  // items
   }
   su_end<D>(bars, tmem, warp, lane);
@@ -552,58 +553,58 @@ attn_sums_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     int i = 0, j = 0, t = 0;
     SuItem next = su_item(p, min(su_index(0), items - 1), false);
     for (; su_index(i) < items; ++i) {
-    const SuItem it = next;
-    if (su_index(i + 1) < items) next = su_item(p, su_index(i + 1), false);  // (its length arrives meanwhile)
-    const SuRow R(p, it.len);
-    const SuSums w(p, it, R);
-    if (w.n == 0) continue;
-    const int key0 = w.key0, key = key0 + row;
-    float total = 0.f;
-    if (grp == 0) ok = su_a_to_tmem<D>(bars, smem, tmem, j, row, lane, p.status) && ok;
-    int q0 = R.lo + w.run0 * SU_RUN, h = grp;  // position of the run's first query
-    for (int k = t + grp; k < t + w.n; k += 2, h += 2) {
-      const int st = k % L::NST, sb = k % L::NS;
-      while (h >= p.rep) { h -= p.rep; q0 += SU_RUN; }
-      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->full + st, (uint32_t)(k / L::NST) & 1u, &bars->abort_flag,
-                                                       p.status));
-      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->s_full + sb, (uint32_t)(k / L::NS) & 1u, &bars->abort_flag,
-                                                       p.status));
-      const float4* ls = reinterpret_cast<const float4*>(smem + L::LSE + st * SU_RUN * 4);
-      auto tile = [&](auto edge) {
-        float s[64];
-        su_scores(s, tmem + lane_base + L::TM_S + sb * SU_RUN);
-        if (lane == 0) tc::mbar_arrive(bars->s_empty + sb);
-        float a4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 e = ls[c >> 2];
-          fma2(s[c], s[c + 1], sc, e.x, e.y);
-          fma2(s[c + 2], s[c + 3], sc, e.z, e.w);
-          float y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            y[i] = ex2f(s[c + i]);
-            if (edge.value) y[i] = q0 + c + i < key || q0 + c + i >= R.n ? 0.f : y[i];
+      const SuItem it = next;
+      if (su_index(i + 1) < items) next = su_item(p, su_index(i + 1), false);  // (its length arrives meanwhile)
+      const SuRow R(p, it.len);
+      const SuSums w(p, it, R);
+      if (w.n == 0) continue;
+      const int key0 = w.key0, key = key0 + row;
+      float total = 0.f;
+      if (grp == 0) ok = su_a_to_tmem<D>(bars, smem, tmem, j, row, lane, p.status) && ok;
+      int q0 = R.lo + w.run0 * SU_RUN, h = grp;  // position of the run's first query
+      for (int k = t + grp; k < t + w.n; k += 2, h += 2) {
+        const int st = k % L::NST, sb = k % L::NS;
+        while (h >= p.rep) { h -= p.rep; q0 += SU_RUN; }
+        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->full + st, (uint32_t)(k / L::NST) & 1u, &bars->abort_flag,
+                                                         p.status));
+        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(bars->s_full + sb, (uint32_t)(k / L::NS) & 1u, &bars->abort_flag,
+                                                         p.status));
+        const float4* ls = reinterpret_cast<const float4*>(smem + L::LSE + st * SU_RUN * 4);
+        auto tile = [&](auto edge) {
+          float s[64];
+          su_scores(s, tmem + lane_base + L::TM_S + sb * SU_RUN);
+          if (lane == 0) tc::mbar_arrive(bars->s_empty + sb);
+          float a4[4] = {0.f, 0.f, 0.f, 0.f};
+  #pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const float4 e = ls[c >> 2];
+            fma2(s[c], s[c + 1], sc, e.x, e.y);
+            fma2(s[c + 2], s[c + 3], sc, e.z, e.w);
+            float y[4];
+  #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              y[i] = ex2f(s[c + i]);
+              if (edge.value) y[i] = q0 + c + i < key || q0 + c + i >= R.n ? 0.f : y[i];
+            }
+            add2(a4[0], a4[1], y[0], y[1]);
+            add2(a4[2], a4[3], y[2], y[3]);
           }
-          add2(a4[0], a4[1], y[0], y[1]);
-          add2(a4[2], a4[3], y[2], y[3]);
-        }
-        total += (a4[0] + a4[1]) + (a4[2] + a4[3]);
-      };
-      // edge: queries before the key, and rows behind the sequence (whatever they hold)
-      if (q0 < key0 + SU_KEYS || q0 + SU_RUN > R.n)
-        tile(SuBool<true>{});
-      else
-        tile(SuBool<false>{});
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bars->empty + st);
-    }
-    t += w.n;
-    ++j;
-    float* x = xch + (j & 1) * 128 + row;  // (in turn: the last item's may still be read)
-    if (grp == 1) *x = total;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (grp == 0 && ok && key < R.n) p.weights[(long long)it.pair * p.w_stride + key] = total + *x;
+          total += (a4[0] + a4[1]) + (a4[2] + a4[3]);
+        };
+        // edge: queries before the key, and rows behind the sequence (whatever they hold)
+        if (q0 < key0 + SU_KEYS || q0 + SU_RUN > R.n)
+          tile(SuBool<true>{});
+        else
+          tile(SuBool<false>{});
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bars->empty + st);
+      }
+      t += w.n;
+      ++j;
+      float* x = xch + (j & 1) * 128 + row;  // (in turn: the last item's may still be read)
+      if (grp == 1) *x = total;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (grp == 0 && ok && key < R.n) p.weights[(long long)it.pair * p.w_stride + key] = total + *x;
     }  // items
   }
   pdl_wait();  // (a CTA without items too: what follows this launch takes the one before it for done)
