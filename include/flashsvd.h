@@ -337,7 +337,9 @@ FLASHSVD_API int flashsvd_prefill_attn_factorized(const flashsvd_bf16* z_q, cons
  * is the least integer with max |x| <= LIM 2^e (LIM = 127 for int8, 448 for
  * e4m3), and at least -100; code = x / 2^e rounded to nearest, ties to even;
  * value = code * 2^e.  A block that holds an infinity or a NaN gets the
- * scale NaN and codes 0 (everything that reads it becomes NaN).  A block is
+ * scale NaN and codes 0 (everything that reads it becomes NaN).  (Finite rows
+ * above 0.96 * 2^128 may get a code whose value is 2^128, which counts as an
+ * infinity when flashsvd_kv8_evict moves the row.)  A block is
  * quantised once, when its 64th row arrives; the rows of the block that
  * holds the newest token are (also) kept in a bf16 tail, and attention reads
  * that block from the tail.  The cache after n rows is therefore the same

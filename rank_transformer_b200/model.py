@@ -72,7 +72,8 @@ class DecoderModel:
                  kv_window: int = 64, max_positions: int | None = None):
         """``kv_format`` ("int8" or "e4m3"): 8-bit key/value caches of S_max
         tokens (a multiple of 64) instead of the bf16 ones; decode then runs
-        the per-stage kernels.  ``kv_keep``: when a cache is full, ``generate``
+        the per-stage kernels (with a single sequence slower than the bf16
+        model's fused one below about 20,000 tokens).  ``kv_keep``: when a cache is full, ``generate``
         evicts every head's tokens down to this many, the ``kv_recent`` newest
         and those with the largest accumulated attention weight (the prompt's
         tokens start with their weight from its last ``kv_window`` queries).

@@ -137,3 +137,25 @@ def test_a_full_model_refuses_a_step(fs):
     torch.cuda.synchronize()
     fs.check_device_status()
     assert m.length == 71 and m.seqlens.tolist() == [71, 71] and m.positions.tolist() == [129, 129]
+
+
+@pytest.mark.parametrize("fmt,code", [("int8", 64.0), ("e4m3", 256.0)])
+def test_a_code_worth_2_to_128_moves_as_an_infinity(fs, fmt, code):
+    """The last bf16 number's code stands for 2^128, which no bf16 row holds:
+    the block that it is moved into gets the scale NaN, as with an infinity."""
+    from rank_transformer_b200.kv8 import KV8Cache
+    n, keep, D = 200, 130, 64
+    x = torch.ones((1, n, 1, D), device="cuda").to(torch.bfloat16)
+    x[0, 5] = torch.finfo(torch.bfloat16).max
+    src, dst = KV8Cache(1, 1, D, 256, fmt), KV8Cache(1, 1, D, 192, fmt)
+    fs.kv8_store(x, x, src, None, n, n)
+    assert src.k.float()[0, 0, 5, 0] == code and torch.isfinite(src.k_scale).all()
+    w = torch.ones((1, 1, 256), device="cuda")
+    w[0, 0, 5] = 2.0
+    wo, kept = torch.zeros((1, 1, 192), device="cuda"), torch.zeros((1, 1, keep), dtype=torch.int32, device="cuda")
+    fs.kv8_evict(src, dst, w, wo, torch.tensor([n], dtype=torch.int32, device="cuda"), None, kept, keep, 0)
+    torch.cuda.synchronize()
+    fs.check_device_status()
+    for s in (dst.k_scale, dst.v_scale):
+        assert torch.isnan(s[0, 0, 0]) and s[0, 0, 1] == (2.0 ** -6 if fmt == "int8" else 2.0 ** -8)
+    assert not dst.k.float()[0, 0, :64].any()
