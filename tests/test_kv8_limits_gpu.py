@@ -159,3 +159,61 @@ def test_a_code_worth_2_to_128_moves_as_an_infinity(fs, fmt, code):
     for s in (dst.k_scale, dst.v_scale):
         assert torch.isnan(s[0, 0, 0]) and s[0, 0, 1] == (2.0 ** -6 if fmt == "int8" else 2.0 ** -8)
     assert not dst.k.float()[0, 0, :64].any()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_caches_beyond_32_bits(fs, fmt):
+    """The last head's rows lie 2^32 bytes and more behind the first one's:
+    stored, attended over, evicted in place and into another cache."""
+    from rank_transformer_b200.kv8 import KV8Cache
+    from tests.test_kv8_gpu import _check_cache
+    n, G, D, S_max, keep = 300, 9, 128, 1 << 22, 130
+    s = _Step(fs, fmt, [n], G, 1, D, S_max, 71, scale=D ** -0.5)
+    c = s.cache
+    assert (G - 1) * S_max * D >= 1 << 32
+    w = torch.full((1, G, S_max), 2.0, device="cuda")
+    s.check(s.run(w), w, 2.0)
+    w[0, :, :n + 1] = torch.rand((G, n + 1), generator=torch.Generator("cuda").manual_seed(5), device="cuda")
+    wh = w[0, :, :n + 1].double().cpu().numpy()
+    seq = torch.tensor([n + 1], dtype=torch.int32, device="cuda")
+    kept = torch.zeros((1, G, keep), dtype=torch.int32, device="cuda")
+    small = KV8Cache(1, G, D, 192, fmt)
+    for dst, wo in ((small, torch.zeros((1, G, 192), device="cuda")), (c, w)):
+        fs.kv8_evict(c, dst, w, wo, seq, None, kept, keep, 20)
+        torch.cuda.synchronize()
+        fs.check_device_status()
+        host = [dict(codes=a[:, :, :192].float().cpu().double().numpy(), scale=x[:, :, :3].cpu().double().numpy(),
+                     tail=t.cpu().double().numpy()) for a, x, t in ((dst.k, dst.k_scale, dst.k_tail),
+                                                                   (dst.v, dst.v_scale, dst.v_tail))]
+        for g in range(G):
+            idx = oracle.evict_kept(wh[g], keep, 20)
+            assert kept[0, g].tolist() == idx.tolist()
+            np.testing.assert_array_equal(wo[0, g, :keep].double().cpu().numpy(), wh[g][idx])
+            for i, rows in enumerate((s.k, s.v)):
+                held = oracle.kv8_rows(rows[0, :, g], fmt)[idx]
+                if dst is small:
+                    old = [{k: np.zeros_like(v) for k, v in h.items()} for h in host]
+                else:     # what lies behind the kept rows stays
+                    old = [{k: v.copy() for k, v in h.items()} for h in host]
+                _check_cache(host, old, i, 0, g, held, fmt)
+
+
+def test_weight_sums_beyond_32_bits(fs):
+    """The window's queries and the last keys lie beyond 2^32 bytes."""
+    S, H, D, window = 70000, 256, 128, 64
+    assert (S - window) * H * D * 2 > 1 << 32
+    g = torch.Generator("cuda").manual_seed(9)
+    q, k = (torch.empty((1, S, H, D), dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    w = torch.zeros((1, H, S), device="cuda")
+    fs.attn_weight_sums(q, k, w, None, 1, S, H, H, D, S, S, window, D ** -0.5)
+    torch.cuda.synchronize()
+    fs.check_device_status()
+    hidden = torch.arange(S, device="cuda")[None, :] > torch.arange(S - window, S, device="cuda")[:, None]
+    for h in (0, 1, 100, 254, 255):
+        qd, kd = q[0, S - window:, h].double(), k[0, :, h].double()
+        want = torch.softmax((qd @ kd.T * D ** -0.5).masked_fill(hidden, -float("inf")), -1).sum(0)
+        # the bound of test_kv8_gpu._sums_bound
+        d = D ** -0.5 * float((qd.abs() @ kd.abs().amax(0)).max()) * (D + 24) * 2 * U32
+        bound = want * (2 * d + 2.0 ** -19 + (S / 4 + 64) * 2 * U32) + 1e-30
+        err = (w[0, h].double() - want).abs()
+        assert (err <= bound).all(), (h, float((err / bound).max()))
